@@ -78,6 +78,9 @@ typedef enum { HSTU_MASK_CAUSAL = 0, HSTU_MASK_MFALCON = 1 } hstu_mask_mode;
 #define HSTU_DEVERR_TIMEOUT     0x8  /* a bounded pipeline wait expired */
 #define HSTU_DEVERR_SL_TOO_LONG 0x10 /* Stochastic Length: a sequence to sub-sample is longer
                                         than HSTU_SL_MAX_SAMPLED_LEN (it is dropped) */
+#define HSTU_DEVERR_PAGES       0x20 /* paged history: a page index outside the pool, a position
+                                        outside a user's row of the page table, a length outside
+                                        it, or several rows of a user in an appending step */
 
 typedef struct {
   int32_t d_model;          /* d = num_heads * head_dim; BF16 compute: 128, 256, 384, 512, 768

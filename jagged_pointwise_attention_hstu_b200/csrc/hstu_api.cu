@@ -10,6 +10,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 #include <utility>
 #include <vector>
@@ -317,7 +318,28 @@ struct LayerRows {
   int num_pairs;           // query-tile pairs listed in `order`
   const int32_t* order;
   const int64_t* ts;       // [T_attn]
+  // rows of a paged step: the attention reads this layer's pages instead
+  const hstu::PagesArgs* pages = nullptr;
+  bool append = false;     // and the rows are written to them
 };
+
+// The attention of rows over pages (and, when appending, their write) on the
+// U|V|Q|K of the workspace: what stands in for the attention kernel of a layer.
+cudaError_t pages_layer(hstu_handle* h, const LayerRows& R, const hstu_layer_weights* w,
+                        cudaStream_t st) {
+  hstu::PagesArgs p = *R.pages;
+  p.uvqk = R.uvqk;
+  p.rab_pos = w->rab_pos;
+  p.rab_time = w->rab_time;
+  p.av = h->ws.av;
+  if (R.append) {
+    Timed tm(h, kBlock, st);
+    const cudaError_t e = hstu::launch_pages_write(p, st);
+    if (e != cudaSuccess) return e;
+  }
+  Timed tm(h, kAttention, st);
+  return hstu::launch_pages_attention(p, st);
+}
 
 LayerRows plain_rows(hstu_handle* h, int64_t T, const int64_t* ts) {
   LayerRows r;
@@ -381,7 +403,9 @@ hstu_status run_layer(hstu_handle* h, const void* x, const LayerRows& R,
                                 4 * d, d, hstu::Epi::kSiluSplit, w->b1,
                                 static_cast<float*>(ws.uvqk), nullptr, st);
     }
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && R.pages != nullptr) {
+      e = pages_layer(h, R, w, st);
+    } else if (e == cudaSuccess) {
       Timed tm(h, kAttention, st);
       e = hstu::launch_attention_f32(a, st);
     }
@@ -422,7 +446,9 @@ hstu_status run_layer(hstu_handle* h, const void* x, const LayerRows& R,
     Timed tm(h, kF1, st);
     e = hstu::launch_gemm_tc(g1, h->num_sms, st, ws.error);
   }
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && R.pages != nullptr) {
+    e = pages_layer(h, R, w, st);
+  } else if (e == cudaSuccess) {
     Timed tm(h, kAttention, st);
     e = hstu::launch_attention_tc(a, st, false);
   }
@@ -1370,3 +1396,230 @@ extern "C" hstu_status hstu_layer_backward(
   if (e == cudaSuccess) e = gemm_f32(h, b.dyt, b.gt, d, d, int(T64), b.zeros, gr->w2, st);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
+
+// ---------------------------------------------------------------------------
+// Paged history
+namespace {
+
+// Makes the handle's device current for a call and the caller's again after it.
+struct DeviceGuard {
+  int before = -1;
+  bool ok = false;
+  explicit DeviceGuard(int device) {
+    if (cudaGetDevice(&before) != cudaSuccess) return;
+    ok = before == device || cudaSetDevice(device) == cudaSuccess;
+    if (before == device) before = -1;
+  }
+  ~DeviceGuard() {
+    if (before >= 0) cudaSetDevice(before);
+  }
+};
+
+hstu_status check_pool(const hstu_handle* h, const hstu_page_pool* p, bool need_ts) {
+  if (p == nullptr) return HSTU_ERR_INVALID_ARG;
+  if (p->format != HSTU_PAGES_BF16 && p->format != HSTU_PAGES_FP32 && p->format != HSTU_PAGES_E4M3)
+    return HSTU_ERR_INVALID_ARG;
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) != 0 ||
+      p->num_pages < 1)
+    return HSTU_ERR_INVALID_ARG;
+  if (p->kv == nullptr || !hstu::aligned16(p->kv)) return HSTU_ERR_INVALID_ARG;
+  if (p->format == HSTU_PAGES_E4M3 && (p->scales == nullptr || !hstu::aligned16(p->scales)))
+    return HSTU_ERR_INVALID_ARG;
+  if ((need_ts && p->timestamps == nullptr) || !hstu::aligned16(p->timestamps))
+    return HSTU_ERR_INVALID_ARG;
+  if ((h->cfg.compute_dtype == HSTU_DTYPE_FP32) != (p->format == HSTU_PAGES_FP32))
+    return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+// The rows and tables of a call; R = 0 needs no pointers.
+hstu_status check_page_rows(const hstu_handle* h, int64_t R, const int32_t* offsets, int32_t B,
+                            const int32_t* table, int32_t width, int32_t page_size) {
+  if (R < 0 || B < 0 || (B == 0 && R != 0)) return HSTU_ERR_INVALID_ARG;
+  if (R > h->cfg.max_tokens || B > h->cfg.max_users) return HSTU_ERR_WORKSPACE;
+  if (R == 0) return HSTU_OK;
+  if (offsets == nullptr || table == nullptr || width < 1) return HSTU_ERR_INVALID_ARG;
+  if (int64_t(width) * page_size > (int64_t(1) << 30)) return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+hstu_status check_ptrs(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p == nullptr || !hstu::aligned16(p)) return HSTU_ERR_INVALID_ARG;
+  return HSTU_OK;
+}
+
+hstu::PagesArgs pages_args(const hstu_handle* h, const hstu_page_pool& p, int64_t R,
+                           const int32_t* offsets, int32_t B, const int64_t* ts,
+                           const int32_t* table, int32_t width, const int32_t* lengths) {
+  const hstu_config& c = h->cfg;
+  hstu::PagesArgs a;
+  memset(&a, 0, sizeof(a));
+  a.format = p.format;
+  while ((1 << a.page_shift) < p.page_size) ++a.page_shift;
+  a.num_pages = p.num_pages;
+  a.kv = p.kv;
+  a.scales = p.scales;
+  a.page_ts = p.timestamps;
+  a.table = table;
+  a.width = width;
+  a.lengths = lengths;
+  a.offsets = offsets;
+  a.B = B;
+  a.R = R;
+  a.ts = ts;
+  a.thresholds = h->ws.thresholds;
+  a.time_lut = h->ws.time_lut;
+  a.thr32 = h->ws.thr32;
+  a.d = c.d_model;
+  a.H = c.num_heads;
+  a.hd = c.head_dim;
+  a.pos_clamp = c.pos_clamp;
+  a.time_buckets = c.time_buckets;
+  a.lut_exact = c.time_log_div > 0.2232 ? 1 : 0;
+  a.n_norm = c.n_norm;
+  a.error = h->ws.error;
+  a.num_sms = h->num_sms;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+hstu_status hstu_pages_write(hstu_handle* h, const hstu_page_pool* pool, const void* uvqk,
+                             int64_t R, const int32_t* offsets, int32_t B, const int64_t* ts,
+                             const int32_t* table, int32_t width, const int32_t* start,
+                             void* stream) {
+  if (h == nullptr) return HSTU_ERR_INVALID_ARG;
+  hstu_status s = check_pool(h, pool, ts != nullptr);
+  if (s == HSTU_OK) s = check_page_rows(h, R, offsets, B, table, width, pool->page_size);
+  if (s != HSTU_OK) return s;
+  if (R == 0) return HSTU_OK;
+  s = check_ptrs({uvqk});
+  if (s != HSTU_OK || !hstu::aligned16(ts)) return HSTU_ERR_INVALID_ARG;
+  const DeviceGuard guard(h->device);
+  if (!guard.ok) return HSTU_ERR_CUDA;
+  hstu::PagesArgs a = pages_args(h, *pool, R, offsets, B, ts, table, width, start);
+  a.uvqk = uvqk;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Timed tm(h, kBlock, st);
+  return hstu::launch_pages_write(a, st) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+hstu_status hstu_pages_read(hstu_handle* h, const hstu_page_pool* pool, const int32_t* table,
+                            int32_t width, const int32_t* start, const int32_t* offsets,
+                            int32_t B, int64_t R, void* uvqk, int64_t* ts, void* stream) {
+  if (h == nullptr) return HSTU_ERR_INVALID_ARG;
+  hstu_status s = check_pool(h, pool, ts != nullptr);
+  if (s == HSTU_OK) s = check_page_rows(h, R, offsets, B, table, width, pool->page_size);
+  if (s != HSTU_OK) return s;
+  if (R == 0) return HSTU_OK;
+  s = check_ptrs({uvqk});
+  if (s != HSTU_OK || !hstu::aligned16(ts)) return HSTU_ERR_INVALID_ARG;
+  const DeviceGuard guard(h->device);
+  if (!guard.ok) return HSTU_ERR_CUDA;
+  hstu::PagesArgs a = pages_args(h, *pool, R, offsets, B, nullptr, table, width, start);
+  a.out = uvqk;
+  a.ts_out = ts;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Timed tm(h, kBlock, st);
+  return hstu::launch_pages_read(a, st) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+hstu_status hstu_pages_attention(hstu_handle* h, const hstu_page_pool* pool, const void* uvqk,
+                                 int64_t R, const int32_t* offsets, int32_t B, const int64_t* ts,
+                                 const int32_t* table, int32_t width, const int32_t* lengths,
+                                 const float* rab_pos, const float* rab_time, float* av,
+                                 void* stream) {
+  if (h == nullptr) return HSTU_ERR_INVALID_ARG;
+  hstu_status s = check_pool(h, pool, true);
+  if (s == HSTU_OK) s = check_page_rows(h, R, offsets, B, table, width, pool->page_size);
+  if (s != HSTU_OK) return s;
+  if (h->cfg.n_norm <= 0) return HSTU_ERR_UNSUPPORTED;
+  if (R == 0) return HSTU_OK;
+  s = check_ptrs({uvqk, ts, rab_pos, rab_time, av});
+  if (s != HSTU_OK || lengths == nullptr) return HSTU_ERR_INVALID_ARG;
+  const DeviceGuard guard(h->device);
+  if (!guard.ok) return HSTU_ERR_CUDA;
+  hstu::PagesArgs a = pages_args(h, *pool, R, offsets, B, ts, table, width, lengths);
+  a.uvqk = uvqk;
+  a.rab_pos = rab_pos;
+  a.rab_time = rab_time;
+  a.av = av;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Timed tm(h, kAttention, st);
+  return hstu::launch_pages_attention(a, st) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+}
+
+hstu_status hstu_pages_prefill(hstu_handle* h, const hstu_page_pool* pools, const void* values,
+                               int64_t T, const int32_t* offsets, int32_t B, const int64_t* ts,
+                               const hstu_layer_weights* layers, int32_t num_layers,
+                               const int32_t* table, int32_t width, void* out, void* stream) {
+  hstu_status s = check_common(h, values, T, offsets, B, ts, HSTU_MASK_CAUSAL, nullptr, out);
+  if (s != HSTU_OK) return s;
+  if (h->cfg.n_norm <= 0) return HSTU_ERR_UNSUPPORTED;
+  if (pools == nullptr || layers == nullptr || num_layers < 1) return HSTU_ERR_INVALID_ARG;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    s = check_weights(&layers[l]);
+    if (s == HSTU_OK) s = check_pool(h, &pools[l], true);
+    if (s == HSTU_OK) s = check_page_rows(h, T, offsets, B, table, width, pools[l].page_size);
+    if (s != HSTU_OK) return s;
+  }
+  if (T == 0) return HSTU_OK;
+  const DeviceGuard guard(h->device);
+  if (!guard.ok) return HSTU_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  {
+    Timed tm(h, kSchedule, st);
+    if (hstu::launch_schedule(h, T, offsets, B, ts, HSTU_MASK_CAUSAL, nullptr, st) != cudaSuccess)
+      return HSTU_ERR_CUDA;
+  }
+  h->last_T = T;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    s = run_layer(h, l == 0 ? values : out, plain_rows(h, T, ts), &layers[l], out, st, l > 0,
+                  l + 1 < num_layers);
+    if (s != HSTU_OK) return s;
+    hstu::PagesArgs a = pages_args(h, pools[l], T, offsets, B, ts, table, width, nullptr);
+    a.uvqk = h->ws.uvqk;
+    Timed tm(h, kBlock, st);
+    if (hstu::launch_pages_write(a, st) != cudaSuccess) return HSTU_ERR_CUDA;
+  }
+  return HSTU_OK;
+}
+
+hstu_status hstu_pages_step(hstu_handle* h, const hstu_page_pool* pools, const void* values,
+                            int64_t R, const int32_t* offsets, int32_t B, const int64_t* ts,
+                            const hstu_layer_weights* layers, int32_t num_layers,
+                            const int32_t* table, int32_t width, const int32_t* lengths,
+                            int32_t append, void* out, void* stream) {
+  if (h == nullptr || pools == nullptr || layers == nullptr || num_layers < 1)
+    return HSTU_ERR_INVALID_ARG;
+  hstu_status s = HSTU_OK;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    s = check_weights(&layers[l]);
+    if (s == HSTU_OK) s = check_pool(h, &pools[l], true);
+    if (s == HSTU_OK) s = check_page_rows(h, R, offsets, B, table, width, pools[l].page_size);
+    if (s != HSTU_OK) return s;
+  }
+  if (h->cfg.n_norm <= 0) return HSTU_ERR_UNSUPPORTED;
+  if (R == 0) return HSTU_OK;
+  s = check_ptrs({values, ts, out});
+  if (s != HSTU_OK || lengths == nullptr) return HSTU_ERR_INVALID_ARG;
+  const DeviceGuard guard(h->device);
+  if (!guard.ok) return HSTU_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  h->last_T = R;
+  for (int32_t l = 0; l < num_layers; ++l) {
+    hstu::PagesArgs a = pages_args(h, pools[l], R, offsets, B, ts, table, width, lengths);
+    a.one_row = append != 0 ? 1 : 0;
+    LayerRows rows = plain_rows(h, R, ts);
+    rows.pages = &a;
+    rows.append = append != 0;
+    s = run_layer(h, l == 0 ? values : out, rows, &layers[l], out, st, l > 0, l + 1 < num_layers);
+    if (s != HSTU_OK) return s;
+  }
+  return HSTU_OK;
+}
+
+}  // extern "C"

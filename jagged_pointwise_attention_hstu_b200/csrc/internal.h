@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "../../include/hstu.h"
+#include "../../include/hstu_pages.h"
 
 namespace hstu {
 
@@ -165,6 +166,43 @@ cudaError_t launch_candidate_block(const int32_t* table, const int32_t* hoff, in
 // Block rows back to packed order (padding dropped); to_block must be false.
 cudaError_t launch_candidate_copy(const int32_t* table, int32_t B, int32_t P, int64_t row_bytes,
                                   const void* src, void* dst, bool to_block, cudaStream_t st);
+
+// pages.cu, pages_attn.cu: the paged history
+struct PagesArgs {
+  // the pool of one layer
+  int format;                // hstu_page_format
+  int page_shift;            // log2(page_size)
+  int32_t num_pages;
+  void* kv;                  // [num_pages, H, 2, page_size, hd]
+  uint8_t* scales;           // [num_pages, H, 2, page_size] (E4M3)
+  int64_t* page_ts;          // [num_pages, page_size]
+  // the users: pages and rows
+  const int32_t* table;      // [B, width]
+  int64_t width;
+  const int32_t* lengths;    // [B]: cached rows (attention), first position (write, read; null: 0)
+  const int32_t* offsets;    // [B + 1]
+  int32_t B;
+  int64_t R;
+  const void* uvqk;          // [R, 4d] compute dtype: the rows (write, attention)
+  const int64_t* ts;         // [R], or null (write: page timestamps stay)
+  void* out;                 // [R, 4d] compute dtype (read: K and V columns)
+  int64_t* ts_out;           // [R] or null (read)
+  int one_row;               // write: a user with more than one row is an error
+  // the attention
+  const float* rab_pos;
+  const float* rab_time;
+  const int64_t* thresholds; // [time_buckets]
+  const uint8_t* time_lut;   // [128]
+  const int32_t* thr32;      // [257]
+  int d, H, hd;
+  int pos_clamp, time_buckets, lut_exact, n_norm;
+  float* av;                 // [R, d] fp32
+  int32_t* error;
+  int num_sms;
+};
+cudaError_t launch_pages_write(const PagesArgs& a, cudaStream_t st);
+cudaError_t launch_pages_read(const PagesArgs& a, cudaStream_t st);
+cudaError_t launch_pages_attention(const PagesArgs& a, cudaStream_t st);
 
 // sl.cu: Stochastic Length over a jagged batch
 constexpr int32_t kSlMaxLen = HSTU_SL_MAX_SAMPLED_LEN;   // longest sequence that is sub-sampled

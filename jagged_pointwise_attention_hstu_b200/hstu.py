@@ -17,6 +17,7 @@ from typing import Optional, Sequence
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libhstu.so")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "hstu.h")
+PAGES_HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "hstu_pages.h")
 
 HSTU_OK = 0
 HSTU_ERR_INVALID_ARG = 1
@@ -35,6 +36,12 @@ HSTU_DEVERR_OFFSETS = 0x1
 HSTU_DEVERR_CANDIDATES = 0x2
 HSTU_DEVERR_TIMESTAMPS = 0x4
 HSTU_DEVERR_TIMEOUT = 0x8
+
+HSTU_DEVERR_PAGES = 0x20
+
+HSTU_PAGES_BF16 = 0
+HSTU_PAGES_FP32 = 1
+HSTU_PAGES_E4M3 = 2
 
 HSTU_TENSOR_UVQK = 0
 HSTU_TENSOR_AV = 1
@@ -65,6 +72,11 @@ class hstu_layer_weights(ctypes.Structure):
     _fields_ = [("w1", c_void_p), ("b1", c_void_p), ("w2", c_void_p), ("b2", c_void_p),
                 ("ln_gamma", c_void_p), ("ln_beta", c_void_p), ("rab_pos", c_void_p),
                 ("rab_time", c_void_p)]
+
+
+class hstu_page_pool(ctypes.Structure):
+    _fields_ = [("format", c_int), ("page_size", c_int32), ("num_pages", c_int32),
+                ("kv", c_void_p), ("scales", c_void_p), ("timestamps", c_void_p)]
 
 
 _lib = None
@@ -123,6 +135,19 @@ def load() -> ctypes.CDLL:
                                         c_void_p, c_int32, c_void_p,
                                         POINTER(hstu_layer_weights), c_int, c_void_p, c_void_p,
                                         POINTER(hstu_layer_grads), c_void_p]),
+        "hstu_pages_write": (c_int, [H, POINTER(hstu_page_pool), c_void_p, c_int64, c_void_p,
+                                     c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+        "hstu_pages_read": (c_int, [H, POINTER(hstu_page_pool), c_void_p, c_int32, c_void_p,
+                                    c_void_p, c_int32, c_int64, c_void_p, c_void_p, c_void_p]),
+        "hstu_pages_attention": (c_int, [H, POINTER(hstu_page_pool), c_void_p, c_int64, c_void_p,
+                                         c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_void_p]),
+        "hstu_pages_prefill": (c_int, [H, POINTER(hstu_page_pool), c_void_p, c_int64, c_void_p,
+                                       c_int32, c_void_p, POINTER(hstu_layer_weights), c_int32,
+                                       c_void_p, c_int32, c_void_p, c_void_p]),
+        "hstu_pages_step": (c_int, [H, POINTER(hstu_page_pool), c_void_p, c_int64, c_void_p,
+                                    c_int32, c_void_p, POINTER(hstu_layer_weights), c_int32,
+                                    c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p]),
         "hstu_set_wait_limit": (c_int, [H, c_int64]),
         "hstu_set_kernel_timing": (c_int, [H, c_int32]),
         "hstu_get_kernel_timing": (c_int, [H, POINTER(c_double), POINTER(c_int64)]),
@@ -135,9 +160,9 @@ def load() -> ctypes.CDLL:
     return lib
 
 
-def declared_symbols() -> list:
-    """Names of the functions declared in include/hstu.h."""
-    with open(HEADER_PATH) as f:
+def declared_symbols(path: str = HEADER_PATH) -> list:
+    """Names of the functions declared in a header (include/hstu.h)."""
+    with open(path) as f:
         text = f.read()
     return sorted(set(re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(hstu_\w+)\s*\(", text, re.M)))
 
@@ -280,6 +305,70 @@ def hstu_cache_score(handle, cache, values, num_candidates: Sequence[int], times
     _check(load().hstu_cache_score(handle, cache, _ptr(values), counts, _ptr(timestamps), arr,
                                    len(layers), _ptr(out), _stream_ptr(stream)),
            "hstu_cache_score")
+
+
+def hstu_page_pool_of(format: int, page_size: int, num_pages: int, kv, scales,
+                      timestamps) -> hstu_page_pool:
+    """The pages of one layer: kv [num_pages, H, 2, page_size, head_dim], scales uint8
+    [num_pages, H, 2, page_size] (E4M3, else None), timestamps int64 [num_pages, page_size]."""
+    return hstu_page_pool(format, page_size, num_pages, _ptr(kv), _ptr(scales), _ptr(timestamps))
+
+
+def hstu_pages_write(handle, pool: hstu_page_pool, uvqk, total_rows: int, seq_offsets,
+                     num_users: int, timestamps, page_table, table_width: int, start=None,
+                     stream=None) -> None:
+    _check(load().hstu_pages_write(handle, pool, _ptr(uvqk), total_rows, _ptr(seq_offsets),
+                                   num_users, _ptr(timestamps), _ptr(page_table), table_width,
+                                   _ptr(start), _stream_ptr(stream)),
+           "hstu_pages_write")
+
+
+def hstu_pages_read(handle, pool: hstu_page_pool, page_table, table_width: int, start,
+                    seq_offsets, num_users: int, total_rows: int, uvqk, timestamps=None,
+                    stream=None) -> None:
+    _check(load().hstu_pages_read(handle, pool, _ptr(page_table), table_width, _ptr(start),
+                                  _ptr(seq_offsets), num_users, total_rows, _ptr(uvqk),
+                                  _ptr(timestamps), _stream_ptr(stream)),
+           "hstu_pages_read")
+
+
+def hstu_pages_attention(handle, pool: hstu_page_pool, uvqk, total_rows: int, seq_offsets,
+                         num_users: int, timestamps, page_table, table_width: int, lengths,
+                         rab_pos, rab_time, av, stream=None) -> None:
+    _check(load().hstu_pages_attention(handle, pool, _ptr(uvqk), total_rows, _ptr(seq_offsets),
+                                       num_users, _ptr(timestamps), _ptr(page_table),
+                                       table_width, _ptr(lengths), _ptr(rab_pos),
+                                       _ptr(rab_time), _ptr(av), _stream_ptr(stream)),
+           "hstu_pages_attention")
+
+
+def _pools(pools: Sequence[hstu_page_pool], layers: Sequence[hstu_layer_weights], what: str):
+    if len(pools) != len(layers):
+        raise HstuError(HSTU_ERR_INVALID_ARG, f"{what}: {len(pools)} pools, {len(layers)} layers")
+    return (hstu_page_pool * len(pools))(*pools), (hstu_layer_weights * len(layers))(*layers)
+
+
+def hstu_pages_prefill(handle, pools: Sequence[hstu_page_pool], values, total_rows: int,
+                       seq_offsets, num_users: int, timestamps,
+                       layers: Sequence[hstu_layer_weights], page_table, table_width: int, out,
+                       stream=None) -> None:
+    ps, ls = _pools(pools, layers, "hstu_pages_prefill")
+    _check(load().hstu_pages_prefill(handle, ps, _ptr(values), total_rows, _ptr(seq_offsets),
+                                     num_users, _ptr(timestamps), ls, len(layers),
+                                     _ptr(page_table), table_width, _ptr(out),
+                                     _stream_ptr(stream)),
+           "hstu_pages_prefill")
+
+
+def hstu_pages_step(handle, pools: Sequence[hstu_page_pool], values, total_rows: int, seq_offsets,
+                    num_users: int, timestamps, layers: Sequence[hstu_layer_weights], page_table,
+                    table_width: int, lengths, append: bool, out, stream=None) -> None:
+    ps, ls = _pools(pools, layers, "hstu_pages_step")
+    _check(load().hstu_pages_step(handle, ps, _ptr(values), total_rows, _ptr(seq_offsets),
+                                  num_users, _ptr(timestamps), ls, len(layers), _ptr(page_table),
+                                  table_width, _ptr(lengths), 1 if append else 0, _ptr(out),
+                                  _stream_ptr(stream)),
+           "hstu_pages_step")
 
 
 HSTU_SL_MAX_SAMPLED_LEN = 8192

@@ -175,5 +175,138 @@ class Handle:
         return hstu.hstu_get_device_error(self.h)
 
 
+_PAGE_FORMAT = {"bf16": hstu.HSTU_PAGES_BF16, "fp32": hstu.HSTU_PAGES_FP32,
+                "e4m3": hstu.HSTU_PAGES_E4M3}
+_PAGE_DTYPE = {"bf16": torch.bfloat16, "fp32": torch.float32, "e4m3": torch.uint8}
+
+
+class PagedHistory:
+    """Histories of up to ``max_users`` users (slots 0 .. max_users - 1) of a stack in pages.
+
+    Owns one pool per layer, the page table, the lengths and the free list; the
+    computing is in the library.  Calls run on the current stream of the
+    handle's device.  ``fmt``: "bf16" or "e4m3" (bf16 compute), "fp32" (fp32 compute).
+    """
+
+    def __init__(self, handle: Handle, layers: List[DeviceLayer], num_pages: int,
+                 max_users: int, pages_per_user: int, page_size: int = 64, fmt: str = "bf16"):
+        c = handle.cfg
+        self.handle, self.layers, self.page_size, self.fmt = handle, layers, page_size, fmt
+        dev = self.device = torch.device("cuda", handle.device)
+        shape = (num_pages, c.num_heads, 2, page_size, c.head_dim)
+        self.kv = [torch.zeros(shape, dtype=_PAGE_DTYPE[fmt], device=dev) for _ in layers]
+        self.scales = [torch.full(shape[:-1], 127, dtype=torch.uint8, device=dev)
+                       if fmt == "e4m3" else None for _ in layers]
+        self.timestamps = torch.zeros((num_pages, page_size), dtype=torch.int64, device=dev)
+        self.pools = [hstu.hstu_page_pool_of(_PAGE_FORMAT[fmt], page_size, num_pages, kv, s,
+                                             self.timestamps)
+                      for kv, s in zip(self.kv, self.scales)]
+        self.structs = [l.struct() for l in layers]
+        self.table = torch.full((max_users, pages_per_user), -1, dtype=torch.int32, device=dev)
+        self.lengths = torch.zeros(max_users, dtype=torch.int32, device=dev)
+        self.held = [0] * max_users                       # lengths, on the host
+        self.pages: List[List[int]] = [[] for _ in range(max_users)]
+        self.free = list(range(num_pages - 1, -1, -1))
+
+    def _reserve(self, want: dict) -> None:
+        """Gives every slot of ``want`` {slot: length} the pages of that length, or none at all."""
+        new = {u: -(-n // self.page_size) - len(self.pages[u]) for u, n in want.items()}
+        if any(len(self.pages[u]) + k > self.table.shape[1] for u, k in new.items()):
+            raise RuntimeError("a history is longer than its row of the page table")
+        if sum(max(k, 0) for k in new.values()) > len(self.free):
+            raise RuntimeError("no free pages")
+        for u, k in new.items():
+            if k > 0:
+                got = [self.free.pop() for _ in range(k)]
+                at = len(self.pages[u])
+                self.table[u, at:at + k] = torch.tensor(got, dtype=torch.int32)
+                self.pages[u] += got
+
+    def _offsets(self, counts: List[int]) -> torch.Tensor:
+        off = np.concatenate([[0], np.cumsum(np.asarray(counts, np.int64))]).astype(np.int32)
+        return torch.from_numpy(off).to(self.device)
+
+    def _slots(self, slots) -> List[int]:
+        slots = [int(u) for u in slots]
+        if len(set(slots)) != len(slots) or any(not 0 <= u < len(self.held) for u in slots):
+            raise ValueError("slots are distinct numbers below max_users")
+        return slots
+
+    def prefill(self, slots, counts, x: torch.Tensor, timestamps: torch.Tensor,
+                out: torch.Tensor) -> torch.Tensor:
+        """Runs the stack over the histories of empty ``slots`` (``counts`` rows each, packed in
+        ``x``) and keeps them."""
+        slots, counts = self._slots(slots), [int(n) for n in counts]
+        if len(counts) != len(slots) or any(n < 0 for n in counts) or sum(counts) != x.shape[0]:
+            raise ValueError("one count a slot, x.shape[0] rows in all")
+        if any(self.held[u] for u in slots):
+            raise ValueError("a prefilled slot has to be empty: release it first")
+        self._reserve(dict(zip(slots, counts)))
+        idx = torch.tensor(slots, dtype=torch.int64, device=self.device)
+        table = self.table[idx].contiguous()
+        hstu.hstu_pages_prefill(self.handle.h, self.pools, x, x.shape[0], self._offsets(counts),
+                                len(slots), timestamps, self.structs, table, table.shape[1], out,
+                                torch.cuda.current_stream(self.device))
+        self.lengths[idx] = torch.tensor(counts, dtype=torch.int32, device=self.device)
+        for u, n in zip(slots, counts):
+            self.held[u] = n
+        return out
+
+    def _step(self, counts, x, timestamps, out, append: bool) -> torch.Tensor:
+        hstu.hstu_pages_step(self.handle.h, self.pools, x, x.shape[0], self._offsets(counts),
+                             len(self.held), timestamps, self.structs, self.table,
+                             self.table.shape[1], self.lengths, append, out,
+                             torch.cuda.current_stream(self.device))
+        return out
+
+    def append(self, slots, x: torch.Tensor, timestamps: torch.Tensor,
+               out: torch.Tensor) -> torch.Tensor:
+        """One new action for each of ``slots`` (ascending): row i of ``x`` is slots[i]'s."""
+        slots = self._slots(slots)
+        if slots != sorted(slots) or len(slots) != x.shape[0]:
+            raise ValueError("ascending slots, one row each")
+        self._reserve({u: self.held[u] + 1 for u in slots})
+        counts = [0] * len(self.held)
+        for u in slots:
+            counts[u] = 1
+        self._step(counts, x, timestamps, out, True)
+        self.lengths += torch.tensor(counts, dtype=torch.int32, device=self.device)
+        for u in slots:
+            self.held[u] += 1
+        return out
+
+    def score(self, counts, x: torch.Tensor, timestamps: torch.Tensor,
+              out: torch.Tensor) -> torch.Tensor:
+        """Candidates of every slot (``counts``, one number a slot), packed in slot order."""
+        counts = [int(n) for n in counts]
+        if len(counts) != len(self.held) or any(n < 0 for n in counts) or \
+                sum(counts) != x.shape[0]:
+            raise ValueError("one count a slot, x.shape[0] rows in all")
+        return self._step(counts, x, timestamps, out, False)
+
+    def read(self, layer: int, slots):
+        """(U|V|Q|K rows with the cached V and K and zeros elsewhere, timestamps) of ``slots``."""
+        slots = self._slots(slots)
+        counts = [self.held[u] for u in slots]
+        c, T = self.handle.cfg, sum(counts)
+        dt = torch.float32 if self.fmt == "fp32" else torch.bfloat16
+        uvqk = torch.zeros((T, 4 * c.d_model), dtype=dt, device=self.device)
+        ts = torch.zeros(T, dtype=torch.int64, device=self.device)
+        table = self.table[torch.tensor(slots, dtype=torch.int64, device=self.device)].contiguous()
+        hstu.hstu_pages_read(self.handle.h, self.pools[layer], table, table.shape[1], None,
+                             self._offsets(counts), len(slots), T, uvqk, ts,
+                             torch.cuda.current_stream(self.device))
+        return uvqk, ts
+
+    def release(self, slot: int) -> None:
+        """Gives the slot's pages back."""
+        slot, = self._slots([slot])
+        self.free += reversed(self.pages[slot])
+        self.pages[slot] = []
+        self.held[slot] = 0
+        self.table[slot] = -1
+        self.lengths[slot] = 0
+
+
 def mask_mode_of(w: Workload) -> int:
     return hstu.HSTU_MASK_MFALCON if w.mask == "mfalcon" else hstu.HSTU_MASK_CAUSAL
