@@ -223,6 +223,10 @@ hstu_status hstu_create(const hstu_config* cfg, int32_t device, hstu_handle** ou
   if (e == cudaSuccess) e = hstu::alloc(&ws.thresholds, 256 * 8);
   if (e == cudaSuccess) e = hstu::alloc(&ws.time_lut, 128);
   if (e == cudaSuccess) e = hstu::alloc(&ws.thr32, 257 * 4);
+  const size_t page_blocks = size_t(h->num_sms) * hstu::kPagesBlocksPerSm;
+  if (e == cudaSuccess) e = hstu::alloc(&ws.page_partial, page_blocks * 2 * hstu::kPagesPartial * 4);
+  if (e == cudaSuccess) e = hstu::alloc(&ws.page_tickets, page_blocks * 4);
+  if (e == cudaSuccess) e = cudaMemset(ws.page_tickets, 0, page_blocks * 4);
   if (e == cudaSuccess) e = cudaMemcpy(ws.time_lut, h->time_lut_host, 128, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemcpy(ws.thr32, h->thr32_host, 257 * 4, cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemset(ws.error, 0, 16);
@@ -245,7 +249,7 @@ hstu_status hstu_destroy(hstu_handle* h) {
   Workspace& ws = h->ws;
   void* ptrs[] = {ws.xb, ws.uvqk, ws.av, ws.g, ws.rows, ws.qtile_order, ws.qtile_cost,
                   ws.ktile_order, ws.ktile_cost, ws.counters, ws.error, ws.thresholds,
-                  ws.time_lut, ws.thr32};
+                  ws.time_lut, ws.thr32, ws.page_partial, ws.page_tickets};
   for (void* p : ptrs)
     if (p != nullptr) cudaFree(p);
   hstu::BwdWorkspace& bw = h->bwd;
@@ -1478,6 +1482,8 @@ hstu::PagesArgs pages_args(const hstu_handle* h, const hstu_page_pool& p, int64_
   a.time_buckets = c.time_buckets;
   a.lut_exact = c.time_log_div > 0.2232 ? 1 : 0;
   a.n_norm = c.n_norm;
+  a.partial = h->ws.page_partial;
+  a.tickets = h->ws.page_tickets;
   a.error = h->ws.error;
   a.num_sms = h->num_sms;
   return a;

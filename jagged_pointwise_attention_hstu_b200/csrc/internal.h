@@ -85,6 +85,8 @@ struct Workspace {
   int64_t* thresholds = nullptr;   // [time_buckets] time-bucket thresholds
   uint8_t* time_lut = nullptr;     // [128] bucket at the low edge of each log2 quarter-octave bin
   int32_t* thr32 = nullptr;        // [257] thresholds capped to int32, padded with INT32_MAX
+  float* page_partial = nullptr;   // paged attention: parts of cut segments
+  int32_t* page_tickets = nullptr; // and how many of them arrived (zero between calls)
 };
 
 }  // namespace hstu
@@ -197,9 +199,14 @@ struct PagesArgs {
   int d, H, hd;
   int pos_clamp, time_buckets, lut_exact, n_norm;
   float* av;                 // [R, d] fp32
+  float* partial;            // [num_sms * kPagesBlocksPerSm, 2, kPagesPartial]: parts of cut segments
+  int32_t* tickets;          // [num_sms * kPagesBlocksPerSm]: parts that arrived; zero between calls
+  int min_units;             // fewest units a block takes
   int32_t* error;
   int num_sms;
 };
+constexpr int kPagesBlocksPerSm = 4;
+constexpr int kPagesPartial = 8 * 128;   // most rows of a group * head dim
 cudaError_t launch_pages_write(const PagesArgs& a, cudaStream_t st);
 cudaError_t launch_pages_read(const PagesArgs& a, cudaStream_t st);
 cudaError_t launch_pages_attention(const PagesArgs& a, cudaStream_t st);
