@@ -23,14 +23,17 @@
 //    soon as the product has.  Nothing is staged in shared memory.
 //  * products on mma.sync, whose N = 8 fits a few rows (a tcgen05 tile has 64
 //    rows at least and wants its operands in shared memory, for work that is
-//    bound by the loads).  Scores: rows of q (M) times keys (N); output:
-//    values (M = dimensions) times P (N = rows); the score layout of a lane is
-//    the operand layout of P, so P never leaves its registers.
+//    bound by the loads).  Scores: the 16 rows of the first operand are 8 keys
+//    twice, with the even and the odd pairs of their dimensions, and a row of
+//    q takes two columns, so that the 16 bytes a lane loads of a key are its
+//    operand as they are; key g and query t meet in one lane.
+//  * from the scores to P a lane has a key: bias, scales, SiLU and the split
+//    are done once a key and row.  P goes through 16-bit shared memory into the
+//    second operand of the output product (rows = columns of P, M = dimensions).
 //  * fp32 results from 16-bit operands: q, k and v are exact in bf16 (bf16
 //    pages) or fp16 (e4m3 codes, and q times a power of two), and P is split
-//    into pieces that go through the product as rows of their own: three bf16
-//    pieces (8 + 8 + 8 bits) or two fp16 ones (11 + 11).  One row of the eight
-//    would do for a single query; the pieces take the others.
+//    into pieces that go through the product as columns of their own: three
+//    bf16 pieces (8 + 8 + 8 bits) or two fp16 ones (11 + 11).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -52,7 +55,13 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float silu(float s) { return __fdividef(s, 1.0f + __expf(-s)); }
+// s / (1 + exp(-s)); exp(-s) above fp32 gives -0, below it s.
+__device__ __forceinline__ float silu(float s) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return s * r;
+}
 
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
@@ -81,27 +90,25 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t two) {   // exact
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(two), __NV_E4M3);
-  return uint32_t(h.x) | (uint32_t(h.y) << 16);
+// Four e4m3 codes as fp16, exactly.
+__device__ __forceinline__ void halves_of_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// What a variant of the kernel is made of.  NT: tiles of 8 operand rows.
+// What a variant of the kernel is made of.  NT: tiles of 8 columns of P.
 template <int FMT, int HD, int NT>
 struct Shape {
   static constexpr bool kF32 = FMT == HSTU_PAGES_FP32;
   static constexpr bool kF16 = FMT == HSTU_PAGES_E4M3;
   static constexpr int kPieces = kF32 ? 1 : (kF16 ? 2 : 3);
-  static constexpr int kGroup = kF32 ? NT : 8 * NT / kPieces;   // rows of q a segment holds
-  static constexpr int kRows = kF32 ? NT : 8 * NT;              // rows of its sums
+  static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 2 * NT);   // rows of q of a segment
+  static constexpr int kTiles = (kGroup + 3) / 4;               // of 4 rows of q, for the scores
+  static constexpr int kRows = kF32 ? NT : 8 * NT;              // columns of P, rows of the sums
   static constexpr int kBlocks = (kF32 || (HD == 128 && !kF16)) ? 1 : 2;   // of 16 keys, a warp's step
   static constexpr int kStep = 16 * kBlocks;                    // keys of a warp's step
   static constexpr int kUnit = kWarps * kStep;                  // keys of a unit
@@ -154,10 +161,12 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
     pages_attention_kernel(const PagesArgs a) {
   using S = Shape<FMT, HD, NT>;
   constexpr int NB = S::kBlocks;
+  static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kRows, "operand");
   __shared__ Shared sh;
   __shared__ int4 s_time[128];                       // per bin: next threshold, two table entries
   __shared__ float s_sum[kWarps][S::kRows][S::kPad];
-  __shared__ float s_bias[kWarps][S::kGroup][S::kStep];
+  // P of a warp's step, a row per column of the operand
+  __shared__ __align__(16) uint16_t s_p[S::kF32 ? 1 : kWarps][S::kRows][S::kStep + 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
 
@@ -263,26 +272,19 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
       }
     }
 
-    // ---- the bias of the step's keys, a lane a key, for every row of the group
-    float (*bias)[S::kStep] = s_bias[warp];
     const int64_t ts0 = __ldg(a.ts + row0);
-    auto write_bias = [&](int32_t j, bool ok, int64_t then) {
-      float pos = pos_far;
-      if (n - j < a.pos_clamp) pos = __ldg(a.rab_pos + (ok ? n - j : 0));
-      for (int q = 0; q < nq; ++q) {
-        const uint64_t now = uint64_t(q == 0 ? ts0 : __ldg(a.ts + row0 + q));
-        const int64_t gap = int64_t(now - uint64_t(then));
-        float v;
-        if (a.lut_exact && gap < 0x7FFFFFFE) {
-          const uint32_t x = gap > 0 ? uint32_t(gap) + 1u : 1u;
-          const int z = __clz(x);
-          const int4 bin = s_time[(31 - z) * 4 + ((x << z) >> 29 & 3)];
-          v = __int_as_float(gap >= bin.x ? bin.z : bin.y);
-        } else {
-          v = __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
-        }
-        if (S::kStep == 32 || lane < S::kStep) bias[q][lane & (S::kStep - 1)] = v + pos;
+    // the two biases of a row of the group at key j, whose time is `then`
+    auto bias_of = [&](int q, int32_t j, int64_t then) {
+      const float pos = n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
+      const uint64_t now = uint64_t(q == 0 ? ts0 : __ldg(a.ts + row0 + q));
+      const int64_t gap = int64_t(now - uint64_t(then));
+      if (a.lut_exact && gap < 0x7FFFFFFE) {
+        const uint32_t x = gap > 0 ? uint32_t(gap) + 1u : 1u;
+        const int z = __clz(x);
+        const int4 bin = s_time[(31 - z) * 4 + ((x << z) >> 29 & 3)];
+        return pos + __int_as_float(gap >= bin.x ? bin.z : bin.y);
       }
+      return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
     };
     auto page_of = [&](int32_t tile) {   // of the lane's key; -1: no key there
       const int32_t j = tile * S::kUnit + warp * S::kStep + (lane & (S::kStep - 1));
@@ -324,9 +326,9 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
         if (page >= 0) {                 // else no keys here, or a page that is none
           const int32_t jl = j0 + (lane & 15);
           if (mine_p >= 0) then = __ldg(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
-          __syncwarp();
-          write_bias(jl, mine_p >= 0, then);
-          __syncwarp();
+          float bias[NT];                // of the lane's key
+#pragma unroll
+          for (int i = 0; i < NT; ++i) bias[i] = bias_of(i < nq ? i : 0, jl, then);
           const float* base = reinterpret_cast<const float*>(
               static_cast<const char*>(a.kv) + block_at(page, j0) * (HD * S::kElem));
           float4 k[4][E], v[4][E];
@@ -354,8 +356,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
               x += __shfl_xor_sync(0xffffffffu, x, 1);
               x += __shfl_xor_sync(0xffffffffu, x, 2);
               x += __shfl_xor_sync(0xffffffffu, x, 4);
+              const float p = silu(x + __shfl_sync(0xffffffffu, bias[i], 4 * s + k4));
               if (!ok) continue;           // no memory behind the history may reach the sum
-              const float p = silu(x + bias[i < nq ? i : 0][4 * s + k4]);
 #pragma unroll
               for (int e = 0; e < E; ++e) {
                 o[i][4 * e] = fmaf(p, v[s][e].x, o[i][4 * e]);
@@ -385,36 +387,26 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
     } else {
       constexpr int KC = HD * S::kElem / 64;     // 16-byte chunks a lane has of a key
       constexpr int VW = HD * S::kElem / 32;     // words a lane has of a value
-      constexpr int KS = HD / 16;                // steps of 16 dimensions
+      constexpr int KS = HD / 32;                // products a tile of scores takes
       constexpr int MT = HD / 16;                // tiles of 16 dimensions of the output
-      // q: rows g and g + 8 of the operand; row r is piece r % kPieces of query r / kPieces
-      uint32_t qa[KS][4];
-      float q_scale[2];
-      float mask1[2], mask2[2];                  // 1: the row's piece is behind the first / second
-      int q_at[2];
+      constexpr int QT = S::kTiles;
+      // Columns 2i and 2i + 1 of the score product are query i, with the even and the odd
+      // pairs of its dimensions: what the lane's g is, at its t's dimensions.
+      uint32_t qb[QT][KS][2];
+      float q_scale[QT];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = g + 8 * half;
-        const int q = r / S::kPieces < nq ? r / S::kPieces : nq - 1;
-        q_at[half] = q;
-        mask1[half] = r % S::kPieces >= 1 ? 1.f : 0.f;
-        mask2[half] = r % S::kPieces >= 2 ? 1.f : 0.f;
-        q_scale[half] = 1.f;
-        if (half >= NT) {
-#pragma unroll
-          for (int s = 0; s < KS; ++s) qa[s][1] = qa[s][3] = 0u;
-          continue;
-        }
+      for (int i = 0; i < QT; ++i) {
+        const int q = 4 * i + (g >> 1) < nq ? 4 * i + (g >> 1) : nq - 1;
+        const bool odd = (g & 1) != 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(a.uvqk) + (row0 + q) * 4 * a.d + 2 * a.d + h * HD);
+        q_scale[i] = 1.f;
         if constexpr (!S::kF16) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const uint4 v = __ldg(src + t + 4 * c);
-            qa[2 * c][half] = v.x;
-            qa[2 * c][half + 2] = v.y;
-            qa[2 * c + 1][half] = v.z;
-            qa[2 * c + 1][half + 2] = v.w;
+            qb[i][c][0] = odd ? v.y : v.x;
+            qb[i][c][1] = odd ? v.w : v.z;
           }
         } else {
           // fp16 of q * 2^-e with |q| below 2^15: bf16's 8 bits are exact down to 2^-32 of the
@@ -426,29 +418,37 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
             unpack_bf16(__ldg(src + 2 * (t + 4 * c)), x[c]);
             unpack_bf16(__ldg(src + 2 * (t + 4 * c) + 1), x[c] + 8);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[c][i]));
+            for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(x[c][k]));
           }
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           int e = int(__float_as_uint(m) >> 23) - 127 - 14;
           e = e < -126 ? -126 : (e > 112 ? 112 : e);
-          q_scale[half] = __int_as_float((e + 127) << 23);
+          q_scale[i] = __int_as_float((e + 127) << 23);
           const float inv = __int_as_float((127 - e) << 23);
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              qa[4 * c + w][half] = pack_half(x[c][4 * w] * inv, x[c][4 * w + 1] * inv);
-              qa[4 * c + w][half + 2] = pack_half(x[c][4 * w + 2] * inv, x[c][4 * w + 3] * inv);
-            }
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const int at = 8 * k + 4 * w;
+                qb[i][2 * c + k][w] = pack_half((odd ? x[c][at + 2] : x[c][at]) * inv,
+                                                (odd ? x[c][at + 3] : x[c][at + 1]) * inv);
+              }
         }
       }
+      uint16_t (*ps)[S::kStep + 8] = s_p[warp];
+      __syncwarp();
+      for (int i = lane; i < S::kRows * (S::kStep + 8) / 2; i += 32)
+        reinterpret_cast<uint32_t*>(&ps[0][0])[i] = 0u;   // columns without a piece
       float acc[MT][NT][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-      // fp16 pieces: P is kept below 2^15 by a power of two of its row (inv), raised when needed
+      // fp16 pieces: P times a power of two of its row stays below 2^15; inv is that of the row
+      // whose two pieces are the lane's columns (row t of the tile)
       float inv[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) inv[i] = __int_as_float((127 + 126) << 23);
@@ -481,32 +481,36 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
           }
         }
       };
-      // values of the keys 2t, 2t + 1, 2t + 8, 2t + 9: the lane's columns of P
+      // values of the keys 4t .. 4t + 3 of each block: the lane's rows of P
       auto load_v = [&](int32_t tile, int32_t p) {
         const int32_t j0 = tile * S::kUnit + warp * S::kStep;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int32_t page = __shfl_sync(0xffffffffu, p, 16 * nb);
           if (page < 0) continue;
-          const char* at = kv + (block_at(page, j0 + 16 * nb) + plane) * (HD * S::kElem);
+          const char* at = kv + (block_at(page, j0 + 16 * nb) + plane + 4 * t) * (HD * S::kElem) +
+                           (VW == 2 ? 8 : 16) * g;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const char* row = at + (2 * t + (i & 1) + 8 * (i >> 1)) * (HD * S::kElem);
+            const char* row = at + i * (HD * S::kElem);
             if constexpr (VW == 2) {
-              const uint2 v = load8(row + 8 * g);
+              const uint2 v = load8(row);
               vr[nb][i][0] = v.x, vr[nb][i][1] = v.y;
             } else {
 #pragma unroll
               for (int c = 0; c < VW / 4; ++c) {
-                const uint4 v = load16(row + 16 * g + 128 * c);
+                const uint4 v = load16(row + 128 * c);
                 vr[nb][i][4 * c] = v.x, vr[nb][i][4 * c + 1] = v.y;
                 vr[nb][i][4 * c + 2] = v.z, vr[nb][i][4 * c + 3] = v.w;
               }
             }
-            if (j0 + 16 * nb + 16 > n && j0 + 16 * nb + 2 * t + (i & 1) + 8 * (i >> 1) >= n) {
+          }
+          if (j0 + 16 * nb + 16 > n) {             // rows behind the history: 0 * NaN
 #pragma unroll
-              for (int w = 0; w < VW; ++w) vr[nb][i][w] = 0u;   // rows behind the history: 0 * NaN
-            }
+            for (int i = 0; i < 4; ++i)
+              if (j0 + 16 * nb + 4 * t + i >= n)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) vr[nb][i][w] = 0u;
           }
         }
       };
@@ -514,19 +518,15 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
       auto fold = [&]() {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          float s0 = 1.f, s1 = 1.f;      // the scales of rows 2t and 2t + 1
-          if constexpr (S::kF16) {
-            s0 = 1.f / __shfl_sync(0xffffffffu, inv[i], 8 * t);
-            s1 = 1.f / __shfl_sync(0xffffffffu, inv[i], 8 * t + 4);
-          }
+          const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
           const int r = 8 * i + 2 * t;
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             const int dim = (S::kF16 ? g * (HD / 8) + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3));
             float2* p0 = reinterpret_cast<float2*>(&sum[r][dim]);
             float2* p1 = reinterpret_cast<float2*>(&sum[r + 1][dim]);
-            float2 x0 = make_float2(acc[m][i][0] * s0, acc[m][i][2] * s0);
-            float2 x1 = make_float2(acc[m][i][1] * s1, acc[m][i][3] * s1);
+            float2 x0 = make_float2(acc[m][i][0] * scale, acc[m][i][2] * scale);
+            float2 x1 = make_float2(acc[m][i][1] * scale, acc[m][i][3] * scale);
             if (folded) {
               const float2 y0 = *p0, y1 = *p1;
               x0.x += y0.x, x0.y += y0.y, x1.x += y1.x, x1.y += y1.y;
@@ -545,146 +545,130 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
       int32_t p_next = page_of(tile0 + 1);
       for (int32_t tile = tile0; tile < tile1; ++tile) {
         const int32_t j0 = tile * S::kUnit + warp * S::kStep;
+        const int32_t jl = j0 + (lane & (S::kStep - 1));      // the lane's key
         int32_t page[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) page[nb] = __shfl_sync(0xffffffffu, p_now, 16 * nb);
-        __syncwarp();
-        write_bias(j0 + (lane & (S::kStep - 1)), p_now >= 0, then);
         const float ks_now = ks, vs_now = vs;
-        float s[NB][2][4];
+        const int64_t then_now = then;
+        float s[NB][2][QT];              // of key 16 nb + 8 x + g and row 4i + t
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          if (page[nb] < 0) continue;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            s[nb][x][0] = s[nb][x][1] = s[nb][x][2] = s[nb][x][3] = 0.f;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-              const uint4 k = kr[nb][x][c];
+            for (int i = 0; i < QT; ++i) s[nb][x][i] = 0.f;
+            if (page[nb] < 0) continue;
+            float c[QT][4];
+#pragma unroll
+            for (int i = 0; i < QT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KC; ++k) {
+              const uint4 v = kr[nb][x][k];
               if constexpr (S::kF16) {
-                const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  mma<true>(s[nb][x], qa[4 * c + i][0], qa[4 * c + i][1], qa[4 * c + i][2],
-                            qa[4 * c + i][3], half2_of_e4m3(w[i] & 0xffffu),
-                            half2_of_e4m3(w[i] >> 16));
+                for (int y = 0; y < 2; ++y) {
+                  uint32_t a0, a1, a2, a3;
+                  halves_of_e4m3(w[2 * y], a0, a1);
+                  halves_of_e4m3(w[2 * y + 1], a2, a3);
+#pragma unroll
+                  for (int i = 0; i < QT; ++i)
+                    mma<true>(c[i], a0, a1, a2, a3, qb[i][2 * k + y][0], qb[i][2 * k + y][1]);
+                }
               } else {
-                mma<false>(s[nb][x], qa[2 * c][0], qa[2 * c][1], qa[2 * c][2], qa[2 * c][3], k.x,
-                           k.y);
-                mma<false>(s[nb][x], qa[2 * c + 1][0], qa[2 * c + 1][1], qa[2 * c + 1][2],
-                           qa[2 * c + 1][3], k.z, k.w);
+#pragma unroll
+                for (int i = 0; i < QT; ++i)
+                  mma<false>(c[i], v.x, v.y, v.z, v.w, qb[i][k][0], qb[i][k][1]);
               }
             }
+#pragma unroll
+            for (int i = 0; i < QT; ++i) s[nb][x][i] = c[i][0] + c[i][3];
           }
         }
         load_k(tile + 1, p_next);
         const int32_t p_then = page_of(tile + 2);
-        __syncwarp();
-        uint32_t pb[NB][NT][2];
+        __syncwarp();                    // the last step's P has been read
+        for (int q = 0; q < nq; ++q) {   // a lane a key
+          float y = 0.f;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (page[nb] < 0) continue;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {            // keys 8x + 2t, 8x + 2t + 1 of the block
-            const int key = 16 * nb + 8 * x + 2 * t;
-            float k0 = 1.f, k1 = 1.f, v0 = 1.f, v1 = 1.f;
-            if constexpr (S::kF16) {
-              k0 = __shfl_sync(0xffffffffu, ks_now, key);
-              k1 = __shfl_sync(0xffffffffu, ks_now, key + 1);
-              v0 = __shfl_sync(0xffffffffu, vs_now, key);
-              v1 = __shfl_sync(0xffffffffu, vs_now, key + 1);
+          for (int i = 0; i < QT; ++i) {
+            if (QT > 1 && (q >> 2) != i) continue;
+            const int src = 4 * (lane & 7) + (q & 3);
+            const float y0 = __shfl_sync(0xffffffffu, s[0][0][i], src);
+            const float y1 = __shfl_sync(0xffffffffu, s[0][1][i], src);
+            y = lane & 8 ? y1 : y0;
+            if constexpr (NB == 2) {
+              const float y2 = __shfl_sync(0xffffffffu, s[1][0][i], src);
+              const float y3 = __shfl_sync(0xffffffffu, s[1][1][i], src);
+              const float z = lane & 8 ? y3 : y2;
+              y = lane & 16 ? z : y;
             }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const float2 bb = *reinterpret_cast<const float2*>(&bias[q_at[i]][key]);
-              float y0 = s[nb][x][2 * i], y1 = s[nb][x][2 * i + 1];
-              if constexpr (S::kF16) y0 = y0 * q_scale[i] * k0, y1 = y1 * q_scale[i] * k1;
-              y0 = silu(y0 + bb.x);
-              y1 = silu(y1 + bb.y);
-              if constexpr (S::kF16) y0 *= v0, y1 *= v1;
-              if (j0 + 16 * nb + 16 > n) {         // the block that the history ends in
-                y0 = j0 + key < n ? y0 : 0.f;
-                y1 = j0 + key + 1 < n ? y1 : 0.f;
-              }
-              s[nb][x][2 * i] = y0;
-              s[nb][x][2 * i + 1] = y1;
-            }
+            if constexpr (S::kF16)
+              y = y * __shfl_sync(0xffffffffu, q_scale[i], 8 * (q & 3)) * ks_now;
           }
-        }
-        if constexpr (S::kF16) {                   // keep |P| * inv within fp16
-          bool over = false;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-              if (page[nb] >= 0)
-                over |= fmaxf(fmaxf(fabsf(s[nb][0][2 * i]), fabsf(s[nb][0][2 * i + 1])),
-                              fmaxf(fabsf(s[nb][1][2 * i]), fabsf(s[nb][1][2 * i + 1]))) * inv[i] >
-                        32768.f;
-          if (__any_sync(0xffffffffu, over)) {
+          y = silu(y + bias_of(q, jl, then_now));
+          if constexpr (S::kF16) y *= vs_now;
+          y = p_now >= 0 ? y : 0.f;      // no key here: what memory holds must not reach the sum
+          if constexpr (S::kF16) {
+            float f = 1.f;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-              float m = 0.f;
+              if (NT > 1 && (q >> 2) != i) continue;
+              f = __shfl_sync(0xffffffffu, inv[i], q & 3);
+              if (__any_sync(0xffffffffu, fabsf(y) * f > 32768.f)) {   // raise the row's power
+                float m = fabsf(y);
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                if (page[nb] >= 0)
-                  m = fmaxf(m, fmaxf(fmaxf(fabsf(s[nb][0][2 * i]), fabsf(s[nb][0][2 * i + 1])),
-                                     fmaxf(fabsf(s[nb][1][2 * i]), fabsf(s[nb][1][2 * i + 1]))));
-              // the row's four lanes, and both pieces of its query
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-              float ratio = 1.f;
-              if (m * inv[i] > 32768.f) {          // to [2^6, 2^7): room to grow
-                int e = int(__float_as_uint(m) >> 23) - 127 - 6;
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                int e = int(__float_as_uint(m) >> 23) - 127 - 6;       // to [2^6, 2^7): room to grow
                 e = e > 126 ? 126 : (e < -126 ? -126 : e);
                 const float now = __int_as_float((127 - e) << 23);
-                ratio = now / inv[i];
-                inv[i] = now;
-              }
-              const float r0 = __shfl_sync(0xffffffffu, ratio, 8 * t);
-              const float r1 = __shfl_sync(0xffffffffu, ratio, 8 * t + 4);
+                const float ratio = now / f;
+                f = now;
+                if (t == (q & 3)) {
+                  inv[i] = now;
 #pragma unroll
-              for (int k = 0; k < MT; ++k) {
-                acc[k][i][0] *= r0, acc[k][i][2] *= r0;
-                acc[k][i][1] *= r1, acc[k][i][3] *= r1;
+                  for (int k = 0; k < MT; ++k) {
+                    acc[k][i][0] *= ratio, acc[k][i][1] *= ratio;
+                    acc[k][i][2] *= ratio, acc[k][i][3] *= ratio;
+                  }
+                }
               }
+            }
+            y *= f;
+            const __half hi = __float2half_rn(y);
+            const __half lo = __float2half_rn(y - __half2float(hi));
+            if (S::kStep == 32 || lane < S::kStep) {
+              ps[2 * q][lane] = __half_as_ushort(hi);
+              ps[2 * q + 1][lane] = __half_as_ushort(lo);
+            }
+          } else {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(y);
+            y -= __bfloat162float(hi);
+            const __nv_bfloat16 mid = __float2bfloat16_rn(y);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(y - __bfloat162float(mid));
+            if (S::kStep == 32 || lane < S::kStep) {
+              ps[3 * q][lane] = __bfloat16_as_ushort(hi);
+              ps[3 * q + 1][lane] = __bfloat16_as_ushort(mid);
+              ps[3 * q + 2][lane] = __bfloat16_as_ushort(lo);
             }
           }
         }
+        __syncwarp();
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if (page[nb] < 0) continue;
+          uint2 pb[NT];                  // P of the keys 4t .. 4t + 3, column g
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {          // the row's piece of P
-              float y0 = s[nb][x][2 * i], y1 = s[nb][x][2 * i + 1];
-              if constexpr (S::kF16) {
-                y0 *= inv[i], y1 *= inv[i];
-                const uint32_t w = pack_half(y0, y1);
-                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                y0 = fmaf(-mask1[i], hi.x, y0), y1 = fmaf(-mask1[i], hi.y, y1);
-                pb[nb][i][x] = pack_half(y0, y1);
-              } else {
-                uint32_t w = pack_bf16(y0, y1);
-                y0 = fmaf(-mask1[i], __uint_as_float(w << 16), y0);
-                y1 = fmaf(-mask1[i], __uint_as_float(w & 0xffff0000u), y1);
-                w = pack_bf16(y0, y1);
-                y0 = fmaf(-mask2[i], __uint_as_float(w << 16), y0);
-                y1 = fmaf(-mask2[i], __uint_as_float(w & 0xffff0000u), y1);
-                pb[nb][i][x] = pack_bf16(y0, y1);
-              }
-            }
+            pb[i] = *reinterpret_cast<const uint2*>(&ps[8 * i + g][16 * nb + 4 * t]);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {           // 16 dimensions: a lane's two neighbours
             uint32_t a0, a1, a2, a3;
             if constexpr (S::kF16) {
               const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
-              const uint32_t x = __byte_perm(vr[nb][0][m >> 1], vr[nb][1][m >> 1], sel);
-              const uint32_t y = __byte_perm(vr[nb][2][m >> 1], vr[nb][3][m >> 1], sel);
-              a0 = half2_of_e4m3(x & 0xffffu), a1 = half2_of_e4m3(x >> 16);
-              a2 = half2_of_e4m3(y & 0xffffu), a3 = half2_of_e4m3(y >> 16);
+              halves_of_e4m3(__byte_perm(vr[nb][0][m >> 1], vr[nb][1][m >> 1], sel), a0, a1);
+              halves_of_e4m3(__byte_perm(vr[nb][2][m >> 1], vr[nb][3][m >> 1], sel), a2, a3);
             } else {
               a0 = __byte_perm(vr[nb][0][m], vr[nb][1][m], 0x5410);
               a1 = __byte_perm(vr[nb][0][m], vr[nb][1][m], 0x7632);
@@ -693,7 +677,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i)
-              mma<S::kF16>(acc[m][i], a0, a1, a2, a3, pb[nb][i][0], pb[nb][i][1]);
+              mma<S::kF16>(acc[m][i], a0, a1, a2, a3, pb[i].x, pb[i].y);
           }
         }
         load_v(tile + 1, p_next);
