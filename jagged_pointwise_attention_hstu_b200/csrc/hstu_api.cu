@@ -528,6 +528,10 @@ hstu_status hstu_get_device_error(hstu_handle* h, int32_t* bits) {
   if (cudaMemcpy(&v, h->ws.error, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return HSTU_ERR_CUDA;
   if (cudaMemset(h->ws.error, 0, 4) != cudaSuccess) return HSTU_ERR_CUDA;
   *bits = v;
+  // a paged attention that gave up may have left parts counted
+  if ((v & HSTU_DEVERR_TIMEOUT) &&
+      cudaMemset(h->ws.page_tickets, 0, size_t(h->num_sms) * hstu::kPagesBlocksPerSm * 4) != cudaSuccess)
+    return HSTU_ERR_CUDA;
   if (v & HSTU_DEVERR_TIMEOUT) return HSTU_ERR_TIMEOUT;
   return v ? HSTU_ERR_DEVICE_CHECK : HSTU_OK;
 }
@@ -1484,6 +1488,7 @@ hstu::PagesArgs pages_args(const hstu_handle* h, const hstu_page_pool& p, int64_
   a.n_norm = c.n_norm;
   a.partial = h->ws.page_partial;
   a.tickets = h->ws.page_tickets;
+  a.wait_limit = h->wait_limit;
   a.error = h->ws.error;
   a.num_sms = h->num_sms;
   return a;

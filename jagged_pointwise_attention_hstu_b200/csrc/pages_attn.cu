@@ -17,16 +17,16 @@
 //    call follows them).  A segment cut between blocks is joined by the last
 //    of them to arrive, in the order of the blocks: same bits every time, no
 //    block waits for another, and one launch does it all.
-//  * a warp takes 16 keys at a time straight from global memory into the
-//    operand layout of the matrix instructions: the next block's keys are
-//    loaded as soon as the scores of this one have used theirs, its values as
-//    soon as the product has.  Nothing is staged in shared memory.
+//  * a producer warp walks the block's units, looks their pages up and fetches
+//    them with bulk copies into a ring of stages in shared memory (a page's
+//    keys and values of a head are one contiguous run), units and segments
+//    ahead of the four warps that compute.
 //  * products on mma.sync, whose N = 8 fits a few rows (a tcgen05 tile has 64
-//    rows at least and wants its operands in shared memory, for work that is
-//    bound by the loads).  Scores: the 16 rows of the first operand are 8 keys
-//    twice, with the even and the odd pairs of their dimensions, and a row of
-//    q takes two columns, so that the 16 bytes a lane loads of a key are its
-//    operand as they are; key g and query t meet in one lane.
+//    rows at least, for work that is bound by the loads).  Scores: the 16 rows
+//    of the first operand are 8 keys twice, with the even and the odd pairs of
+//    their dimensions, and a row of q takes two columns, so that the 16 bytes a
+//    lane reads of a key are its operand as they are; key g and query t meet in
+//    one lane.
 //  * from the scores to P a lane has a key: bias, scales, SiLU and the split
 //    are done once a key and row.  P goes through 16-bit shared memory into the
 //    second operand of the output product (rows = columns of P, M = dimensions).
@@ -34,19 +34,24 @@
 //    pages) or fp16 (e4m3 codes, and q times a power of two), and P is split
 //    into pieces that go through the product as columns of their own: three
 //    bf16 pieces (8 + 8 + 8 bits) or two fp16 ones (11 + 11).
+// fp32 pages (the fp32 path, small models) take the same units with loads
+// straight into registers and fp32 arithmetic.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "pages.cuh"
+#include "sm100.cuh"
 
 namespace hstu {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;       // that compute
 constexpr int kFold = 16;       // matrix products chained before the fp32 sums take over
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -61,18 +66,6 @@ __device__ __forceinline__ float silu(float s) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s * -1.44269504f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return s * r;
-}
-
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ uint2 load8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
 }
 
 template <bool F16>
@@ -109,12 +102,18 @@ struct Shape {
   static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 2 * NT);   // rows of q of a segment
   static constexpr int kTiles = (kGroup + 3) / 4;               // of 4 rows of q, for the scores
   static constexpr int kRows = kF32 ? NT : 8 * NT;              // columns of P, rows of the sums
-  static constexpr int kBlocks = (kF32 || (HD == 128 && !kF16)) ? 1 : 2;   // of 16 keys, a warp's step
+  static constexpr int kRow = HD * (kF32 ? 4 : (kF16 ? 1 : 2)); // bytes of a key
+  static constexpr int kBlocks = !kF32 && kRow == 64 ? 2 : 1;            // of 16 keys, a warp's step
   static constexpr int kStep = 16 * kBlocks;                    // keys of a warp's step
   static constexpr int kUnit = kWarps * kStep;                  // keys of a unit
-  static constexpr int kElem = kF32 ? 4 : (kF16 ? 1 : 2);
-  static constexpr int kPerSm = HD == 128 ? (NT == 2 ? 2 : 3) : (NT == 2 ? 3 : 4);
   static constexpr int kPad = HD + 8;                           // row stride of the sums
+  static constexpr int kThreads = 32 * (kWarps + (kF32 ? 0 : 1));
+  // the ring: a unit's keys and values, scales and times
+  static constexpr int kScalesAt = 2 * kUnit * kRow;
+  static constexpr int kTimesAt = kScalesAt + (kF16 ? 2 * kUnit : 0);
+  static constexpr int kStageBytes = kTimesAt + 8 * kUnit;
+  static constexpr int kStages = kRow == 256 ? 2 : 3;
+  static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT == 2 ? 2 : 3);
 };
 
 struct User {
@@ -148,30 +147,19 @@ __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err)
   return u;
 }
 
-struct Shared {
-  int64_t scan[kWarps];
-  int64_t start;         // first unit of the block's first user
+// The block's run of units [u0, u1), the user it begins in and that user's
+// first unit; by the whole block (two barriers).  False: nothing to do.
+struct Plan {
+  int64_t scan[8];
+  int64_t start, share;
   int32_t user;
-  int32_t last;
-  float self[8];         // SiLU of each row's score with itself
 };
 
-template <int FMT, int HD, int NT>
-__global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
-    pages_attention_kernel(const PagesArgs a) {
-  using S = Shape<FMT, HD, NT>;
-  constexpr int NB = S::kBlocks;
-  static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kRows, "operand");
-  __shared__ Shared sh;
-  __shared__ int4 s_time[128];                       // per bin: next threshold, two table entries
-  __shared__ float s_sum[kWarps][S::kRows][S::kPad];
-  // P of a warp's step, a row per column of the operand
-  __shared__ __align__(16) uint16_t s_p[S::kF32 ? 1 : kWarps][S::kRows][S::kStep + 8];
+template <class S>
+__device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl, int64_t& u0, int64_t& u1) {
+  constexpr int kAll = S::kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
-
-  // ---- the block's units [u0, u1) of all units
-  const int32_t per = (a.B + kWarps * 32 - 1) / (kWarps * 32);
+  const int32_t per = (a.B + kAll - 1) / kAll;
   int err = 0;
   int64_t mine = 0;
   for (int32_t b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += user_of<S>(a, b, err).units;
@@ -181,29 +169,21 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
     const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) sh.scan[warp] = inc;
-  if (tid < 128) {
-    const int cand = __ldg(a.time_lut + tid);
-    const int next = cand + 1 < a.time_buckets ? cand + 1 : a.time_buckets - 1;
-    s_time[tid] = make_int4(cand + 1 < a.time_buckets ? __ldg(a.thr32 + cand + 1) : 0x7FFFFFFF,
-                            __float_as_int(__ldg(a.rab_time + cand)),
-                            __float_as_int(__ldg(a.rab_time + next)), 0);
-  }
+  if (lane == 31) pl.scan[warp] = inc;
+  if (blockIdx.x == 0 && err != 0) atomicOr(a.error, err);
   __syncthreads();
   int64_t before = inc - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sh.scan[w];
-    total += sh.scan[w];
+  for (int w = 0; w < kAll / 32; ++w) {
+    if (w < warp) before += pl.scan[w];
+    total += pl.scan[w];
   }
-  if (blockIdx.x == 0 && err != 0) atomicOr(a.error, err);
-  err = 0;
-  // equal runs, but at least min_units: a cut costs a join (see launch)
+  // equal runs, but at least min_units: a cut costs a join
   int64_t share = (total + gridDim.x - 1) / gridDim.x;
   if (share < a.min_units) share = a.min_units;
-  int64_t u0 = int64_t(blockIdx.x) * share;
-  if (u0 >= total) return;
-  const int64_t u1 = u0 + share < total ? u0 + share : total;
+  u0 = int64_t(blockIdx.x) * share;
+  if (u0 >= total) return false;
+  u1 = u0 + share < total ? u0 + share : total;
   if (u0 >= before && u0 < before + mine) {
     int64_t at = before;
     int32_t b = tid * per;
@@ -213,22 +193,41 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
       if (u0 < at + k) break;
       at += k;
     }
-    sh.start = at;
-    sh.user = b;
+    pl.start = at;
+    pl.user = b;
+    pl.share = share;
   }
   __syncthreads();
-  int32_t b = sh.user;
-  int64_t start = sh.start;
-  User user = user_of<S>(a, b, err);
+  return true;
+}
 
-  const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
-  const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
+// A block's part of one segment: tiles (units) [tile0, tile1) of row group
+// `first` .. `first` + nq - 1 of a user, head h.
+struct Part {
+  int64_t row0;          // the group's first row
+  int32_t h, nq, n;
+  int32_t b;
+  int32_t tile0, tile1;
+  int32_t c0, c1;        // the first and last block that have a part
+};
 
-  while (u0 < u1) {
-    while (u0 >= start + user.units) {   // the next user that has rows
+// Walks the block's run part by part (one warp, or all alike).
+template <class S>
+struct Walk {
+  int64_t u, u1, start, share;
+  int32_t b;
+  User user;
+  __device__ __forceinline__ Walk(const PagesArgs& a, const Plan& pl, int64_t u0, int64_t end)
+      : u(u0), u1(end), start(pl.start), share(pl.share), b(pl.user) {
+    int e = 0;
+    user = user_of<S>(a, b, e);
+  }
+  __device__ __forceinline__ bool next(const PagesArgs& a, Part& p) {
+    if (u >= u1) return false;
+    if (u >= start + user.units) {        // the next user that has rows
       start += user.units;
       for (;;) {
-        const int32_t c = b + 1 + lane;
+        const int32_t c = b + 1 + int32_t(threadIdx.x & 31);
         int e = 0;
         const bool has = c < a.B && user_of<S>(a, c, e).units > 0;
         const unsigned m = __ballot_sync(0xffffffffu, has);
@@ -237,100 +236,179 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
           break;
         }
         b += 32;
-        if (b >= a.B) return;            // cannot happen: u0 < total
+        if (b >= a.B) return false;       // cannot happen: u < total
       }
-      user = user_of<S>(a, b, err);
+      int e = 0;
+      user = user_of<S>(a, b, e);
     }
-    const int64_t rel = u0 - start;
-    const int32_t seg = int32_t(rel / user.nu), tile0 = int32_t(rel - int64_t(seg) * user.nu);
-    const int h = seg % a.H, first = seg / a.H * S::kGroup;
-    const int nq = user.rows - first < S::kGroup ? user.rows - first : S::kGroup;
-    const int64_t row0 = user.r0 + first;
-    const int32_t tile1 = int64_t(user.nu - tile0) < u1 - u0 ? user.nu : int32_t(tile0 + (u1 - u0));
-    const int64_t seg0 = u0 - tile0;     // the segment's first unit
-    const int32_t n = user.n;
-    const int32_t* table = a.table + int64_t(b) * a.width;
+    const int64_t rel = u - start;
+    const int32_t seg = user.units <= INT32_MAX ? int32_t(rel) / user.nu : int32_t(rel / user.nu);
+    const int32_t first = seg / a.H * S::kGroup;
+    p.tile0 = int32_t(rel - int64_t(seg) * user.nu);
+    p.tile1 = int64_t(user.nu - p.tile0) < u1 - u ? user.nu : int32_t(p.tile0 + (u1 - u));
+    p.b = b;
+    p.h = seg % a.H;
+    p.nq = user.rows - first < S::kGroup ? user.rows - first : S::kGroup;
+    p.n = user.n;
+    p.row0 = user.r0 + first;
+    const int64_t seg0 = u - p.tile0;     // the segment's first unit
+    p.c0 = p.tile0 == 0 && p.tile1 == user.nu ? int32_t(blockIdx.x) : int32_t(seg0 / share);
+    p.c1 = p.tile0 == 0 && p.tile1 == user.nu ? p.c0 : int32_t((seg0 + user.nu - 1) / share);
+    u += p.tile1 - p.tile0;
+    return true;
+  }
+};
 
-    // the rows' scores with themselves go with the segment's first unit
-    if (tile0 == 0) {
-      for (int q = warp; q < nq; q += kWarps) {
-        const int64_t at = (row0 + q) * 4 * a.d + 2 * a.d + h * HD + lane;
-        float s = 0.f;
+// rab_time's bins: next threshold, the two table entries it decides between.
+__device__ __forceinline__ void fill_time(const PagesArgs& a, int4* s_time, int k) {
+  const int cand = __ldg(a.time_lut + k);
+  const int next = cand + 1 < a.time_buckets ? cand + 1 : a.time_buckets - 1;
+  s_time[k] = make_int4(cand + 1 < a.time_buckets ? __ldg(a.thr32 + cand + 1) : 0x7FFFFFFF,
+                        __float_as_int(__ldg(a.rab_time + cand)),
+                        __float_as_int(__ldg(a.rab_time + next)), 0);
+}
+
+// The two biases of a row at time `now` for key j at time `then`.
+__device__ __forceinline__ float bias_of(const PagesArgs& a, const int4* s_time, float pos_far,
+                                         int32_t n, int32_t j, int64_t now, int64_t then) {
+  const float pos = n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
+  const int64_t gap = int64_t(uint64_t(now) - uint64_t(then));
+  if (a.lut_exact && gap < 0x7FFFFFFE) {
+    const uint32_t x = gap > 0 ? uint32_t(gap) + 1u : 1u;
+    const int z = __clz(x);
+    const int4 bin = s_time[(31 - z) * 4 + ((x << z) >> 29 & 3)];
+    return pos + __int_as_float(gap >= bin.x ? bin.z : bin.y);
+  }
+  return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
+}
+
+// SiLU of each row's score with itself: a warp a row.
+template <class S, int HD>
+__device__ __forceinline__ void self_scores(const PagesArgs& a, const Part& p, float bias,
+                                            float* self, int& err) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int q = warp; q < p.nq; q += kWarps) {
+    const int64_t at = (p.row0 + q) * 4 * a.d + 2 * a.d + p.h * HD + lane;
+    float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < HD / 32; ++e) {
-          if (S::kF32)
-            s = fmaf(static_cast<const float*>(a.uvqk)[at + 32 * e],
-                     static_cast<const float*>(a.uvqk)[at + a.d + 32 * e], s);
-          else
-            s = fmaf(__bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + 32 * e]),
-                     __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + a.d + 32 * e]), s);
-        }
-        s = warp_sum(s) + self_bias;
-        const int64_t ts = __ldg(a.ts + row0 + q);
-        if (ts < 0 || ts >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
-        if (lane == 0) sh.self[q] = silu(s);
+    for (int e = 0; e < HD / 32; ++e) {
+      if (S::kF32)
+        s = fmaf(static_cast<const float*>(a.uvqk)[at + 32 * e],
+                 static_cast<const float*>(a.uvqk)[at + a.d + 32 * e], s);
+      else
+        s = fmaf(__bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + 32 * e]),
+                 __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + a.d + 32 * e]), s);
+    }
+    s = warp_sum(s) + bias;
+    const int64_t ts = __ldg(a.ts + p.row0 + q);
+    if (ts < 0 || ts >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
+    if (lane == 0) self[q] = silu(s);
+  }
+}
+
+// The warps' sums of a part, by the 128 threads that compute: written out, or
+// left for the last block of the segment, which joins the parts in block order.
+// sync() is a barrier of these threads; it returns false to give up.
+template <class S, int HD, class Sum, class Sync>
+__device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, const Sum& sum,
+                                       const float* self, int32_t* last, Sync sync) {
+  const int tid = threadIdx.x;
+  const bool whole = p.c0 == p.c1;
+  float* part = a.partial + (int64_t(blockIdx.x) * 2 + (p.tile0 == 0 ? 1 : 0)) * (S::kGroup * HD);
+  for (int i = tid; i < p.nq * HD; i += kWarps * 32) {
+    const int q = i / HD, c = i % HD;
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+      for (int k = 0; k < S::kPieces; ++k) x += sum[w][q * S::kPieces + k][c];
+    if (p.tile0 == 0) {
+      const int64_t at = (p.row0 + q) * 4 * a.d + a.d + p.h * HD + c;
+      const float v = S::kF32 ? static_cast<const float*>(a.uvqk)[at]
+                              : __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at]);
+      x = fmaf(self[q], v, x);
+    }
+    if (whole) a.av[(p.row0 + q) * a.d + p.h * HD + c] = x / float(a.n_norm);
+    else part[i] = x;
+  }
+  if (!whole) {
+    __threadfence();
+    if (!sync()) return false;
+    if (tid == 0) {
+      const int32_t k = atomicAdd(a.tickets + p.c0, 1);
+      *last = k == p.c1 - p.c0 ? 1 : 0;
+      if (*last) a.tickets[p.c0] = 0;              // as the next call expects it
+    }
+    if (!sync()) return false;
+    if (*last) {
+      __threadfence();
+      for (int i = tid; i < p.nq * HD; i += kWarps * 32) {
+        float x = 0.f;
+        for (int32_t c = p.c0; c <= p.c1; ++c)
+          x += __ldcg(a.partial + (int64_t(c) * 2 + (c == p.c0 ? 1 : 0)) * (S::kGroup * HD) + i);
+        a.av[(p.row0 + i / HD) * a.d + p.h * HD + i % HD] = x / float(a.n_norm);
       }
     }
+  }
+  return sync();
+}
 
-    const int64_t ts0 = __ldg(a.ts + row0);
-    // the two biases of a row of the group at key j, whose time is `then`
-    auto bias_of = [&](int q, int32_t j, int64_t then) {
-      const float pos = n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
-      const uint64_t now = uint64_t(q == 0 ? ts0 : __ldg(a.ts + row0 + q));
-      const int64_t gap = int64_t(now - uint64_t(then));
-      if (a.lut_exact && gap < 0x7FFFFFFE) {
-        const uint32_t x = gap > 0 ? uint32_t(gap) + 1u : 1u;
-        const int z = __clz(x);
-        const int4 bin = s_time[(31 - z) * 4 + ((x << z) >> 29 & 3)];
-        return pos + __int_as_float(gap >= bin.x ? bin.z : bin.y);
+// fp32 pages: 8 lanes a key, 4 keys at once, fp32 throughout.
+template <int HD, int NT>
+__global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::kPerSm))
+    pages_attention_f32_kernel(const PagesArgs a) {
+  using S = Shape<HSTU_PAGES_FP32, HD, NT>;
+  constexpr int E = HD / 32;
+  __shared__ Plan plan;
+  __shared__ int4 s_time[128];
+  __shared__ float s_sum[kWarps][NT][S::kPad];
+  __shared__ float s_self[8];
+  __shared__ int32_t s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int k4 = lane >> 3, t8 = lane & 7;
+  int64_t u0, u1;
+  fill_time(a, s_time, tid);
+  if (!make_plan<S>(a, plan, u0, u1)) return;
+  Walk<S> walk(a, plan, u0, u1);
+  const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
+  const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
+  const int32_t slot_mask = (1 << a.page_shift) - 1;
+  const int64_t plane = int64_t(1) << a.page_shift;
+  int err = 0;
+  Part p;
+  while (walk.next(a, p)) {
+    const int32_t n = p.n;
+    const int32_t* table = a.table + int64_t(p.b) * a.width;
+    if (p.tile0 == 0) self_scores<S, HD>(a, p, self_bias, s_self, err);
+    float q[NT][4 * E], o[NT][4 * E];
+    int64_t now[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int64_t r = p.row0 + (i < p.nq ? i : 0);
+      now[i] = __ldg(a.ts + r);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.uvqk) +
+                               r * 4 * a.d + 2 * a.d + p.h * HD + 32 * e) + t8);
+        q[i][4 * e] = v.x, q[i][4 * e + 1] = v.y, q[i][4 * e + 2] = v.z, q[i][4 * e + 3] = v.w;
+        o[i][4 * e] = o[i][4 * e + 1] = o[i][4 * e + 2] = o[i][4 * e + 3] = 0.f;
       }
-      return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
-    };
-    auto page_of = [&](int32_t tile) {   // of the lane's key; -1: no key there
-      const int32_t j = tile * S::kUnit + warp * S::kStep + (lane & (S::kStep - 1));
-      if (tile >= tile1 || j >= n) return -1;
-      const int32_t p = __ldg(table + (j >> a.page_shift));
-      if (p >= 0 && p < a.num_pages) return p;
-      err |= HSTU_DEVERR_PAGES;
-      return -1;
-    };
-    const int32_t slot_mask = (1 << a.page_shift) - 1;
-    // block of plane 0 of this head at the first of the 16 keys from j on
-    auto block_at = [&](int32_t page, int32_t j) {
-      return ((((int64_t(page) * a.H + h) * 2) << a.page_shift) + (j & slot_mask));
-    };
-    const int64_t plane = int64_t(1) << a.page_shift;
-
-    int64_t then = 0;
+    }
     float (*sum)[S::kPad] = s_sum[warp];
     bool folded = false;
-
-    if constexpr (S::kF32) {
-      // 8 lanes a key, 4 keys at once, fp32 throughout
-      constexpr int E = HD / 32;
-      const int k4 = lane >> 3, t8 = lane & 7;
-      float q[NT][4 * E], o[NT][4 * E];
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int64_t r = row0 + (i < nq ? i : 0);
-          const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.uvqk) +
-                                 r * 4 * a.d + 2 * a.d + h * HD + 32 * e) + t8);
-          q[i][4 * e] = v.x, q[i][4 * e + 1] = v.y, q[i][4 * e + 2] = v.z, q[i][4 * e + 3] = v.w;
-          o[i][4 * e] = o[i][4 * e + 1] = o[i][4 * e + 2] = o[i][4 * e + 3] = 0.f;
-        }
-      for (int32_t tile = tile0; tile < tile1; ++tile) {
-        const int32_t j0 = tile * S::kUnit + warp * S::kStep;
-        const int32_t mine_p = page_of(tile), page = __shfl_sync(0xffffffffu, mine_p, 0);
-        if (page >= 0) {                 // else no keys here, or a page that is none
-          const int32_t jl = j0 + (lane & 15);
-          if (mine_p >= 0) then = __ldg(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
+    for (int32_t tile = p.tile0; tile < p.tile1; ++tile) {
+      const int32_t j0 = tile * S::kUnit + warp * S::kStep, jl = j0 + (lane & 15);
+      if (j0 < n) {
+        const int32_t page = __ldg(table + (j0 >> a.page_shift));
+        if (page < 0 || page >= a.num_pages) {
+          err |= HSTU_DEVERR_PAGES;
+        } else {
+          const int64_t then = __ldg(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
           float bias[NT];                // of the lane's key
 #pragma unroll
-          for (int i = 0; i < NT; ++i) bias[i] = bias_of(i < nq ? i : 0, jl, then);
-          const float* base = reinterpret_cast<const float*>(
-              static_cast<const char*>(a.kv) + block_at(page, j0) * (HD * S::kElem));
+          for (int i = 0; i < NT; ++i) bias[i] = bias_of(a, s_time, pos_far, n, jl, now[i], then);
+          const float* base = static_cast<const float*>(a.kv) +
+              ((((int64_t(page) * a.H + p.h) * 2) << a.page_shift) + (j0 & slot_mask)) * HD;
           float4 k[4][E], v[4][E];
 #pragma unroll
           for (int s = 0; s < 4; ++s)
@@ -356,50 +434,257 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
               x += __shfl_xor_sync(0xffffffffu, x, 1);
               x += __shfl_xor_sync(0xffffffffu, x, 2);
               x += __shfl_xor_sync(0xffffffffu, x, 4);
-              const float p = silu(x + __shfl_sync(0xffffffffu, bias[i], 4 * s + k4));
-              if (!ok) continue;           // no memory behind the history may reach the sum
+              const float y = silu(x + __shfl_sync(0xffffffffu, bias[i], 4 * s + k4));
+              if (ok) {                  // no memory behind the history may reach the sum
 #pragma unroll
-              for (int e = 0; e < E; ++e) {
-                o[i][4 * e] = fmaf(p, v[s][e].x, o[i][4 * e]);
-                o[i][4 * e + 1] = fmaf(p, v[s][e].y, o[i][4 * e + 1]);
-                o[i][4 * e + 2] = fmaf(p, v[s][e].z, o[i][4 * e + 2]);
-                o[i][4 * e + 3] = fmaf(p, v[s][e].w, o[i][4 * e + 3]);
+                for (int e = 0; e < E; ++e) {
+                  o[i][4 * e] = fmaf(y, v[s][e].x, o[i][4 * e]);
+                  o[i][4 * e + 1] = fmaf(y, v[s][e].y, o[i][4 * e + 1]);
+                  o[i][4 * e + 2] = fmaf(y, v[s][e].z, o[i][4 * e + 2]);
+                  o[i][4 * e + 3] = fmaf(y, v[s][e].w, o[i][4 * e + 3]);
+                }
               }
             }
           }
         }
-        if ((tile - tile0) % kFold == kFold - 1 || tile + 1 == tile1) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4 * E; ++e) {
-              float x = o[i][e] + __shfl_xor_sync(0xffffffffu, o[i][e], 8);
-              x += __shfl_xor_sync(0xffffffffu, x, 16);
-              float* at = &sum[i][(e >> 2) * 32 + 4 * t8 + (e & 3)];
-              if (k4 == 0) *at = folded ? *at + x : x;
-              o[i][e] = 0.f;
-            }
-          folded = true;
-        }
       }
-      if (!folded)
-        for (int i = lane; i < NT * HD; i += 32) sum[i / HD][i % HD] = 0.f;
-    } else {
-      constexpr int KC = HD * S::kElem / 64;     // 16-byte chunks a lane has of a key
-      constexpr int VW = HD * S::kElem / 32;     // words a lane has of a value
-      constexpr int KS = HD / 32;                // products a tile of scores takes
-      constexpr int MT = HD / 16;                // tiles of 16 dimensions of the output
-      constexpr int QT = S::kTiles;
+      if ((tile - p.tile0) % kFold == kFold - 1 || tile + 1 == p.tile1) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4 * E; ++e) {
+            float x = o[i][e] + __shfl_xor_sync(0xffffffffu, o[i][e], 8);
+            x += __shfl_xor_sync(0xffffffffu, x, 16);
+            float* at = &sum[i][(e >> 2) * 32 + 4 * t8 + (e & 3)];
+            if (k4 == 0) *at = folded ? *at + x : x;
+            o[i][e] = 0.f;
+          }
+        folded = true;
+      }
+    }
+    __syncthreads();
+    finish<S, HD>(a, p, s_sum, s_self, &s_last, [] {
+      __syncthreads();
+      return true;
+    });
+  }
+  if (err != 0) atomicOr(a.error, err);
+}
+
+// One unit on its way through the ring.
+struct Unit {
+  Part part;
+  int32_t tile;
+  uint32_t bad;          // runs (below) whose page index is none
+  int32_t stop;
+};
+
+// untiled bulk copy global -> shared; all of dst, src and bytes multiples of 16
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar)) : "memory");
+}
+
+// Waits for a phase for at most `limit` cycles.  The bound is looked at before the first
+// try_wait, which may sleep for longer than a copy takes: a bound of a few cycles gives up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long long limit) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(sm100::smem_u32(bar)), "r"(parity) : "memory");
+  if (ok) return true;
+  const long long t0 = clock64();
+  do {
+    if (clock64() - t0 > limit) return false;
+  } while (!sm100::mbar_try_wait(bar, parity));
+  return true;
+}
+
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+
+template <class S>
+struct Ring {
+  uint64_t full[S::kStages], empty[S::kStages], turn;
+  Unit unit[S::kStages];
+  int32_t last;
+  float self[8];
+};
+
+// A unit's keys lie in runs of run = min(page_size, kUnit) keys, a page each:
+// [run][plane][key] in the stage, as in the pool; its scales [run][plane][key],
+// its times [key].
+template <int FMT, int HD, int NT>
+__global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD, NT>::kPerSm))
+    pages_attention_kernel(const PagesArgs a) {
+  using S = Shape<FMT, HD, NT>;
+  using namespace sm100;
+  constexpr int NB = S::kBlocks;
+  extern __shared__ __align__(128) uint8_t stages[];
+  __shared__ Plan plan;
+  __shared__ Ring<S> ring;
+  __shared__ int4 s_time[128];
+  __shared__ float s_sum[kWarps][S::kRows][S::kPad];
+  // P of a warp's step, a row per column of the operand
+  __shared__ __align__(16) uint16_t s_p[kWarps][S::kRows][S::kStep + 8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long limit = a.wait_limit > 0 ? a.wait_limit : kWaitLimit;
+  int64_t u0, u1;
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&ring.full[s], 1);
+      mbar_init(&ring.empty[s], kWarps);
+    }
+    mbar_init(&ring.turn, kWarps);
+    fence_mbarrier_init();
+  }
+  if (tid < 128) fill_time(a, s_time, tid);
+  if (!make_plan<S>(a, plan, u0, u1)) return;
+  const int32_t run_shift = (1 << a.page_shift) < S::kUnit ? a.page_shift : 31 - __clz(S::kUnit);
+  const int32_t run = 1 << run_shift;
+  int err = 0;
+
+  if (warp == kWarps) {
+    // ---- the producer
+    Walk<S> walk(a, plan, u0, u1);
+    Part p;
+    uint32_t issued = 0;                 // units put into the ring
+    bool ok = true;
+    while (ok && walk.next(a, p)) {
+      const int32_t* table = a.table + int64_t(p.b) * a.width;
+      auto page_of = [&](int32_t tile) { // of the lane's run; -1: no key there, -2: no such page
+        const int64_t j = int64_t(tile) * S::kUnit + (int64_t(lane) << run_shift);
+        if (tile >= p.tile1 || (lane << run_shift) >= S::kUnit || j >= p.n) return -1;
+        const int32_t x = __ldg(table + (j >> a.page_shift));
+        return x >= 0 && x < a.num_pages ? x : -2;
+      };
+      int32_t page_next = page_of(p.tile0);
+      for (int32_t tile = p.tile0; tile < p.tile1; ++tile) {
+        const int32_t page = page_next;
+        page_next = page_of(tile + 1);
+        const int s = issued % S::kStages;
+        if (!wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit)) {
+          ok = false;
+          break;
+        }
+        const int32_t j = tile * S::kUnit + (lane << run_shift);
+        // whole blocks of 16 keys: what lies behind the history in the last one is not used
+        int32_t keys = page >= 0 ? (p.n - j < run ? (p.n - j + 15) & ~15 : run) : 0;
+        const uint32_t per_key = 2 * S::kRow + (S::kF16 ? 2 : 0) + 8;
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, uint32_t(keys) * per_key);
+        const unsigned bad = __ballot_sync(0xffffffffu, page == -2);
+        if (bad != 0) err |= HSTU_DEVERR_PAGES;
+        if (lane == 0) {
+          Unit& u = ring.unit[s];
+          u.part = p;
+          u.tile = tile;
+          u.bad = bad;
+          u.stop = 0;
+          mbar_arrive_expect_tx(&ring.full[s], bytes);
+        }
+        __syncwarp();
+        if (keys > 0) {
+          uint64_t* bar = &ring.full[s];
+          const uint32_t at = smem_u32(stages) + s * S::kStageBytes;
+          const int32_t slot = j & ((1 << a.page_shift) - 1);
+          const int64_t block = (((int64_t(page) * a.H + p.h) * 2) << a.page_shift) + slot;
+          const uint32_t first = lane << (run_shift + 1);       // of the stage's blocks
+          const char* kv = static_cast<const char*>(a.kv) + block * S::kRow;
+          const int64_t plane = int64_t(1) << a.page_shift;
+          bulk_load(at + S::kTimesAt + (lane << run_shift) * 8,
+                    a.page_ts + (int64_t(page) << a.page_shift) + slot, keys * 8, bar);
+          if (keys == 1 << a.page_shift) {                      // a whole page: both planes at once
+            bulk_load(at + first * S::kRow, kv, 2 * keys * S::kRow, bar);
+            if (S::kF16) bulk_load(at + S::kScalesAt + first, a.scales + block, 2 * keys, bar);
+          } else {
+            bulk_load(at + first * S::kRow, kv, keys * S::kRow, bar);
+            bulk_load(at + (first + run) * S::kRow, kv + plane * S::kRow, keys * S::kRow, bar);
+            if (S::kF16) {
+              bulk_load(at + S::kScalesAt + first, a.scales + block, keys, bar);
+              bulk_load(at + S::kScalesAt + first + run, a.scales + block + plane, keys, bar);
+            }
+          }
+        }
+        ++issued;
+      }
+    }
+    const int s = issued % S::kStages;
+    if (ok) ok = wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
+    if (ok && lane == 0) {
+      ring.unit[s].stop = 1;
+      mbar_arrive(&ring.full[s]);
+    }
+    if (!ok) err |= HSTU_DEVERR_TIMEOUT;
+    // no copy may land after the block has gone, whoever gave up
+    for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0; k < issued; ++k)
+      if (k % S::kStages != s || !ok)
+        mbar_wait(&ring.full[k % S::kStages], (k / S::kStages) & 1);
+    if (err != 0) atomicOr(a.error, err);
+    return;
+  }
+
+  // ---- the warps that compute
+  constexpr int KC = S::kRow / 64;             // 16-byte chunks a lane has of a key
+  constexpr int VW = S::kRow / 32;             // words a lane has of a value
+  constexpr int KS = HD / 32;                  // products a tile of scores takes
+  constexpr int MT = HD / 16;                  // tiles of 16 dimensions of the output
+  constexpr int QT = S::kTiles;
+  const int g = lane >> 2, t = lane & 3;
+  const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
+  const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
+  float (*sum)[S::kPad] = s_sum[warp];
+  uint16_t (*ps)[S::kStep + 8] = s_p[warp];
+  uint32_t turn = 0;
+  auto sync = [&]() {                          // of the warps that compute
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.turn);
+    const bool ok = wait_for(&ring.turn, turn, limit);
+    turn ^= 1;
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  uint32_t qb[QT][KS][2];
+  float q_scale[QT], inv[NT], acc[MT][NT][4];
+  int64_t now0 = 0;
+  int folds = 0, chain = 0;
+
+  for (uint32_t k = 0;; ++k) {
+    const int st = k % S::kStages;
+    const bool here = wait_for(&ring.full[st], (k / S::kStages) & 1, limit);
+    if (!__all_sync(0xffffffffu, here)) {
+      err |= HSTU_DEVERR_TIMEOUT;
+      break;
+    }
+    const Unit& unit = ring.unit[st];
+    if (unit.stop) break;
+    const Part& p = unit.part;
+    const int32_t n = p.n, nq = p.nq, tile = unit.tile;
+    const bool end = tile + 1 == p.tile1;
+
+    if (tile == p.tile0) {
+      // ---- a new part: q, and nothing summed
+      if (p.tile0 == 0) self_scores<S, HD>(a, p, self_bias, ring.self, err);
+      now0 = __ldg(a.ts + p.row0);
       // Columns 2i and 2i + 1 of the score product are query i, with the even and the odd
       // pairs of its dimensions: what the lane's g is, at its t's dimensions.
-      uint32_t qb[QT][KS][2];
-      float q_scale[QT];
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
         const int q = 4 * i + (g >> 1) < nq ? 4 * i + (g >> 1) : nq - 1;
         const bool odd = (g & 1) != 0;
         const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.uvqk) + (row0 + q) * 4 * a.d + 2 * a.d + h * HD);
+            static_cast<const __nv_bfloat16*>(a.uvqk) + (p.row0 + q) * 4 * a.d + 2 * a.d + p.h * HD);
         q_scale[i] = 1.f;
         if constexpr (!S::kF16) {
 #pragma unroll
@@ -418,229 +703,137 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
             unpack_bf16(__ldg(src + 2 * (t + 4 * c)), x[c]);
             unpack_bf16(__ldg(src + 2 * (t + 4 * c) + 1), x[c] + 8);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(x[c][k]));
+            for (int y = 0; y < 16; ++y) m = fmaxf(m, fabsf(x[c][y]));
           }
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           int e = int(__float_as_uint(m) >> 23) - 127 - 14;
           e = e < -126 ? -126 : (e > 112 ? 112 : e);
           q_scale[i] = __int_as_float((e + 127) << 23);
-          const float inv = __int_as_float((127 - e) << 23);
+          const float f = __int_as_float((127 - e) << 23);
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
-                const int at = 8 * k + 4 * w;
-                qb[i][2 * c + k][w] = pack_half((odd ? x[c][at + 2] : x[c][at]) * inv,
-                                                (odd ? x[c][at + 3] : x[c][at + 1]) * inv);
+                const int at = 8 * y + 4 * w;
+                qb[i][2 * c + y][w] = pack_half((odd ? x[c][at + 2] : x[c][at]) * f,
+                                                (odd ? x[c][at + 3] : x[c][at + 1]) * f);
               }
         }
       }
-      uint16_t (*ps)[S::kStep + 8] = s_p[warp];
       __syncwarp();
       for (int i = lane; i < S::kRows * (S::kStep + 8) / 2; i += 32)
         reinterpret_cast<uint32_t*>(&ps[0][0])[i] = 0u;   // columns without a piece
-      float acc[MT][NT][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
       // fp16 pieces: P times a power of two of its row stays below 2^15; inv is that of the row
       // whose two pieces are the lane's columns (row t of the tile)
-      float inv[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) inv[i] = __int_as_float((127 + 126) << 23);
+      folds = chain = 0;
+    }
 
-      uint4 kr[NB][2][KC];
-      uint32_t vr[NB][4][VW];
-      float ks = 0.f, vs = 0.f;
-      const char* kv = static_cast<const char*>(a.kv);
-      // keys g and g + 8 of each block; the lane's own key's time and scales
-      auto load_k = [&](int32_t tile, int32_t p) {
-        const int32_t j0 = tile * S::kUnit + warp * S::kStep;
+    const int32_t k0 = warp * S::kStep, j0 = tile * S::kUnit + k0;   // the warp's keys
+    if (j0 < n) {
+      const uint32_t base = smem_u32(stages) + st * S::kStageBytes;
+      // the lane's own key
+      const int32_t kl = k0 + (lane & (S::kStep - 1)), jl = tile * S::kUnit + kl;
+      const bool mine = jl < n && !(unit.bad >> (kl >> run_shift) & 1);
+      const uint2 tw = lds8(base + S::kTimesAt + kl * 8);
+      const int64_t then = int64_t(uint64_t(tw.y) << 32 | tw.x);
+      float ks = 1.f, vs = 1.f;
+      // [run][plane][key]
+      const uint32_t own = ((kl >> run_shift) << (run_shift + 1)) + (kl & (run - 1));
+      if constexpr (S::kF16) {
+        const uint8_t* sc = stages + st * S::kStageBytes + S::kScalesAt + own;
+        ks = block_scale(sc[0]);
+        vs = block_scale(sc[run]);
+      }
+      float s[NB][2][QT];                // of key 16 nb + 8 x + g and row 4i + t
+      uint32_t at[NB];                   // the blocks' first keys
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int32_t page = __shfl_sync(0xffffffffu, p, 16 * nb);
-          if (page < 0) continue;
-          const char* at = kv + (block_at(page, j0 + 16 * nb) + g) * (HD * S::kElem) + 16 * t;
+      for (int nb = 0; nb < NB; ++nb) {
+        const int32_t kb = k0 + 16 * nb;
+        at[nb] = base + (((kb >> run_shift) << (run_shift + 1)) + (kb & (run - 1))) * S::kRow;
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            kr[nb][0][c] = load16(at + 64 * c);
-            kr[nb][1][c] = load16(at + 8 * HD * S::kElem + 64 * c);
-          }
-        }
-        if (p >= 0) {
-          const int32_t j = j0 + (lane & (S::kStep - 1));
-          then = __ldg(a.page_ts + (int64_t(p) << a.page_shift) + (j & slot_mask));
-          if (S::kF16) {
-            const uint8_t* sc = a.scales + block_at(p, j);
-            ks = block_scale(__ldg(sc));
-            vs = block_scale(__ldg(sc + plane));
-          }
-        }
-      };
-      // values of the keys 4t .. 4t + 3 of each block: the lane's rows of P
-      auto load_v = [&](int32_t tile, int32_t p) {
-        const int32_t j0 = tile * S::kUnit + warp * S::kStep;
+        for (int x = 0; x < 2; ++x) {
+          float c[QT][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int32_t page = __shfl_sync(0xffffffffu, p, 16 * nb);
-          if (page < 0) continue;
-          const char* at = kv + (block_at(page, j0 + 16 * nb) + plane + 4 * t) * (HD * S::kElem) +
-                           (VW == 2 ? 8 : 16) * g;
+          for (int i = 0; i < QT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const char* row = at + i * (HD * S::kElem);
-            if constexpr (VW == 2) {
-              const uint2 v = load8(row);
-              vr[nb][i][0] = v.x, vr[nb][i][1] = v.y;
-            } else {
+          for (int y = 0; y < KC; ++y) {
+            const uint4 v = lds16(at[nb] + (8 * x + g) * S::kRow + 64 * y + 16 * t);
+            if constexpr (S::kF16) {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int c = 0; c < VW / 4; ++c) {
-                const uint4 v = load16(row + 128 * c);
-                vr[nb][i][4 * c] = v.x, vr[nb][i][4 * c + 1] = v.y;
-                vr[nb][i][4 * c + 2] = v.z, vr[nb][i][4 * c + 3] = v.w;
-              }
-            }
-          }
-          if (j0 + 16 * nb + 16 > n) {             // rows behind the history: 0 * NaN
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (j0 + 16 * nb + 4 * t + i >= n)
-#pragma unroll
-                for (int w = 0; w < VW; ++w) vr[nb][i][w] = 0u;
-          }
-        }
-      };
-      // acc into the warp's fp32 sums
-      auto fold = [&]() {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
-          const int r = 8 * i + 2 * t;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int dim = (S::kF16 ? g * (HD / 8) + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3));
-            float2* p0 = reinterpret_cast<float2*>(&sum[r][dim]);
-            float2* p1 = reinterpret_cast<float2*>(&sum[r + 1][dim]);
-            float2 x0 = make_float2(acc[m][i][0] * scale, acc[m][i][2] * scale);
-            float2 x1 = make_float2(acc[m][i][1] * scale, acc[m][i][3] * scale);
-            if (folded) {
-              const float2 y0 = *p0, y1 = *p1;
-              x0.x += y0.x, x0.y += y0.y, x1.x += y1.x, x1.y += y1.y;
-            }
-            *p0 = x0;
-            *p1 = x1;
-            acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-          }
-        }
-        folded = true;
-      };
-
-      int32_t p_now = page_of(tile0);
-      load_k(tile0, p_now);
-      load_v(tile0, p_now);
-      int32_t p_next = page_of(tile0 + 1);
-      for (int32_t tile = tile0; tile < tile1; ++tile) {
-        const int32_t j0 = tile * S::kUnit + warp * S::kStep;
-        const int32_t jl = j0 + (lane & (S::kStep - 1));      // the lane's key
-        int32_t page[NB];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) page[nb] = __shfl_sync(0xffffffffu, p_now, 16 * nb);
-        const float ks_now = ks, vs_now = vs;
-        const int64_t then_now = then;
-        float s[NB][2][QT];              // of key 16 nb + 8 x + g and row 4i + t
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-#pragma unroll
-            for (int i = 0; i < QT; ++i) s[nb][x][i] = 0.f;
-            if (page[nb] < 0) continue;
-            float c[QT][4];
-#pragma unroll
-            for (int i = 0; i < QT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
-#pragma unroll
-            for (int k = 0; k < KC; ++k) {
-              const uint4 v = kr[nb][x][k];
-              if constexpr (S::kF16) {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  uint32_t a0, a1, a2, a3;
-                  halves_of_e4m3(w[2 * y], a0, a1);
-                  halves_of_e4m3(w[2 * y + 1], a2, a3);
-#pragma unroll
-                  for (int i = 0; i < QT; ++i)
-                    mma<true>(c[i], a0, a1, a2, a3, qb[i][2 * k + y][0], qb[i][2 * k + y][1]);
-                }
-              } else {
+              for (int z = 0; z < 2; ++z) {
+                uint32_t a0, a1, a2, a3;
+                halves_of_e4m3(w[2 * z], a0, a1);
+                halves_of_e4m3(w[2 * z + 1], a2, a3);
 #pragma unroll
                 for (int i = 0; i < QT; ++i)
-                  mma<false>(c[i], v.x, v.y, v.z, v.w, qb[i][k][0], qb[i][k][1]);
+                  mma<true>(c[i], a0, a1, a2, a3, qb[i][2 * y + z][0], qb[i][2 * y + z][1]);
               }
-            }
+            } else {
 #pragma unroll
-            for (int i = 0; i < QT; ++i) s[nb][x][i] = c[i][0] + c[i][3];
+              for (int i = 0; i < QT; ++i)
+                mma<false>(c[i], v.x, v.y, v.z, v.w, qb[i][y][0], qb[i][y][1]);
+            }
           }
+#pragma unroll
+          for (int i = 0; i < QT; ++i) s[nb][x][i] = c[i][0] + c[i][3];
         }
-        load_k(tile + 1, p_next);
-        const int32_t p_then = page_of(tile + 2);
-        __syncwarp();                    // the last step's P has been read
-        for (int q = 0; q < nq; ++q) {   // a lane a key
-          float y = 0.f;
+      }
+      // Key (lane & 15) of its block is row (key >> 2) of the lane (key & 3)'s four keys
+      const int spot = (lane & 16) + 4 * (lane & 3) + (lane >> 2 & 3);
+      __syncwarp();                      // the last step's P has been read
 #pragma unroll
-          for (int i = 0; i < QT; ++i) {
-            if (QT > 1 && (q >> 2) != i) continue;
-            const int src = 4 * (lane & 7) + (q & 3);
-            const float y0 = __shfl_sync(0xffffffffu, s[0][0][i], src);
-            const float y1 = __shfl_sync(0xffffffffu, s[0][1][i], src);
-            y = lane & 8 ? y1 : y0;
-            if constexpr (NB == 2) {
-              const float y2 = __shfl_sync(0xffffffffu, s[1][0][i], src);
-              const float y3 = __shfl_sync(0xffffffffu, s[1][1][i], src);
-              const float z = lane & 8 ? y3 : y2;
-              y = lane & 16 ? z : y;
-            }
-            if constexpr (S::kF16)
-              y = y * __shfl_sync(0xffffffffu, q_scale[i], 8 * (q & 3)) * ks_now;
+      for (int i = 0; i < QT; ++i) {
+        for (int q = 4 * i; q < nq && q < 4 * i + 4; ++q) {   // a lane a key
+          const int src = 4 * (lane & 7) + (q & 3);
+          const float y0 = __shfl_sync(0xffffffffu, s[0][0][i], src);
+          const float y1 = __shfl_sync(0xffffffffu, s[0][1][i], src);
+          float y = lane & 8 ? y1 : y0;
+          if constexpr (NB == 2) {
+            const float y2 = __shfl_sync(0xffffffffu, s[1][0][i], src);
+            const float y3 = __shfl_sync(0xffffffffu, s[1][1][i], src);
+            const float z = lane & 8 ? y3 : y2;
+            y = lane & 16 ? z : y;
           }
-          y = silu(y + bias_of(q, jl, then_now));
-          if constexpr (S::kF16) y *= vs_now;
-          y = p_now >= 0 ? y : 0.f;      // no key here: what memory holds must not reach the sum
+          if constexpr (S::kF16) y = y * __shfl_sync(0xffffffffu, q_scale[i], 8 * (q & 3)) * ks;
+          const int64_t now = q == 0 ? now0 : __ldg(a.ts + p.row0 + q);
+          y = silu(y + bias_of(a, s_time, pos_far, n, jl, now, then));
+          if constexpr (S::kF16) y *= vs;
+          y = mine ? y : 0.f;            // no key here: what memory holds must not reach the sum
           if constexpr (S::kF16) {
-            float f = 1.f;
+            // e4m3: four rows a tile of scores, and a tile of P
+            float f = __shfl_sync(0xffffffffu, inv[i], q & 3);
+            if (__any_sync(0xffffffffu, fabsf(y) * f > 32768.f)) {   // raise the row's power
+              float m = fabsf(y);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              if (NT > 1 && (q >> 2) != i) continue;
-              f = __shfl_sync(0xffffffffu, inv[i], q & 3);
-              if (__any_sync(0xffffffffu, fabsf(y) * f > 32768.f)) {   // raise the row's power
-                float m = fabsf(y);
+              for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              int e = int(__float_as_uint(m) >> 23) - 127 - 6;       // to [2^6, 2^7): room to grow
+              e = e > 126 ? 126 : (e < -126 ? -126 : e);
+              const float f1 = __int_as_float((127 - e) << 23);
+              const float ratio = t == (q & 3) ? f1 / f : 1.f;
+              if (t == (q & 3)) inv[i] = f1;
+              f = f1;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                int e = int(__float_as_uint(m) >> 23) - 127 - 6;       // to [2^6, 2^7): room to grow
-                e = e > 126 ? 126 : (e < -126 ? -126 : e);
-                const float now = __int_as_float((127 - e) << 23);
-                const float ratio = now / f;
-                f = now;
-                if (t == (q & 3)) {
-                  inv[i] = now;
-#pragma unroll
-                  for (int k = 0; k < MT; ++k) {
-                    acc[k][i][0] *= ratio, acc[k][i][1] *= ratio;
-                    acc[k][i][2] *= ratio, acc[k][i][3] *= ratio;
-                  }
-                }
+              for (int m2 = 0; m2 < MT; ++m2) {
+                acc[m2][i][0] *= ratio, acc[m2][i][1] *= ratio;
+                acc[m2][i][2] *= ratio, acc[m2][i][3] *= ratio;
               }
             }
             y *= f;
             const __half hi = __float2half_rn(y);
             const __half lo = __float2half_rn(y - __half2float(hi));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[2 * q][lane] = __half_as_ushort(hi);
-              ps[2 * q + 1][lane] = __half_as_ushort(lo);
+              ps[2 * q][spot] = __half_as_ushort(hi);
+              ps[2 * q + 1][spot] = __half_as_ushort(lo);
             }
           } else {
             const __nv_bfloat16 hi = __float2bfloat16_rn(y);
@@ -648,102 +841,129 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<FMT, HD, NT>::kPerSm))
             const __nv_bfloat16 mid = __float2bfloat16_rn(y);
             const __nv_bfloat16 lo = __float2bfloat16_rn(y - __bfloat162float(mid));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[3 * q][lane] = __bfloat16_as_ushort(hi);
-              ps[3 * q + 1][lane] = __bfloat16_as_ushort(mid);
-              ps[3 * q + 2][lane] = __bfloat16_as_ushort(lo);
+              ps[3 * q][spot] = __bfloat16_as_ushort(hi);
+              ps[3 * q + 1][spot] = __bfloat16_as_ushort(mid);
+              ps[3 * q + 2][spot] = __bfloat16_as_ushort(lo);
             }
           }
         }
-        __syncwarp();
+      }
+      __syncwarp();
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          if (page[nb] < 0) continue;
-          uint2 pb[NT];                  // P of the keys 4t .. 4t + 3, column g
+      for (int nb = 0; nb < NB; ++nb) {
+        if (j0 + 16 * nb >= n) continue;           // nothing was loaded there
+        uint2 pb[NT];                  // P of the keys t, t + 4, t + 8, t + 12, column g
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          pb[i] = *reinterpret_cast<const uint2*>(&ps[8 * i + g][16 * nb + 4 * t]);
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t row = at[nb] + (run + t + 4 * i) * S::kRow + (VW == 2 ? 8 : 16) * g;
+          if constexpr (VW == 2) {
+            const uint2 x = lds8(row);
+            v[i][0] = x.x, v[i][1] = x.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < VW / 4; ++c) {
+              const uint4 x = lds16(row + 128 * c);
+              v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
+            }
+          }
+        }
+        if (j0 + 16 * nb + 16 > n) {               // rows behind the history: 0 * NaN
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j0 + 16 * nb + t + 4 * i >= n)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) v[i][w] = 0u;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {             // 16 dimensions: a lane's two neighbours
+          uint32_t a0, a1, a2, a3;
+          if constexpr (S::kF16) {
+            const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
+            halves_of_e4m3(__byte_perm(v[0][m >> 1], v[1][m >> 1], sel), a0, a1);
+            halves_of_e4m3(__byte_perm(v[2][m >> 1], v[3][m >> 1], sel), a2, a3);
+          } else {
+            a0 = __byte_perm(v[0][m], v[1][m], 0x5410);
+            a1 = __byte_perm(v[0][m], v[1][m], 0x7632);
+            a2 = __byte_perm(v[2][m], v[3][m], 0x5410);
+            a3 = __byte_perm(v[2][m], v[3][m], 0x7632);
+          }
 #pragma unroll
           for (int i = 0; i < NT; ++i)
-            pb[i] = *reinterpret_cast<const uint2*>(&ps[8 * i + g][16 * nb + 4 * t]);
+            mma<S::kF16>(acc[m][i], a0, a1, a2, a3, pb[i].x, pb[i].y);
+        }
+      }
+    }
+    // ---- the chain of products into the warp's fp32 sums
+    ++chain;
+    if (chain == kFold || end) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {           // 16 dimensions: a lane's two neighbours
-            uint32_t a0, a1, a2, a3;
-            if constexpr (S::kF16) {
-              const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
-              halves_of_e4m3(__byte_perm(vr[nb][0][m >> 1], vr[nb][1][m >> 1], sel), a0, a1);
-              halves_of_e4m3(__byte_perm(vr[nb][2][m >> 1], vr[nb][3][m >> 1], sel), a2, a3);
-            } else {
-              a0 = __byte_perm(vr[nb][0][m], vr[nb][1][m], 0x5410);
-              a1 = __byte_perm(vr[nb][0][m], vr[nb][1][m], 0x7632);
-              a2 = __byte_perm(vr[nb][2][m], vr[nb][3][m], 0x5410);
-              a3 = __byte_perm(vr[nb][2][m], vr[nb][3][m], 0x7632);
-            }
+      for (int i = 0; i < NT; ++i) {
+        const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
+        const int r = 8 * i + 2 * t;
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
-              mma<S::kF16>(acc[m][i], a0, a1, a2, a3, pb[i].x, pb[i].y);
+        for (int m = 0; m < MT; ++m) {
+          const int dim = (S::kF16 ? g * (HD / 8) + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3));
+          float2* p0 = reinterpret_cast<float2*>(&sum[r][dim]);
+          float2* p1 = reinterpret_cast<float2*>(&sum[r + 1][dim]);
+          float2 x0 = make_float2(acc[m][i][0] * scale, acc[m][i][2] * scale);
+          float2 x1 = make_float2(acc[m][i][1] * scale, acc[m][i][3] * scale);
+          if (folds > 0) {
+            const float2 y0 = *p0, y1 = *p1;
+            x0.x += y0.x, x0.y += y0.y, x1.x += y1.x, x1.y += y1.y;
           }
-        }
-        load_v(tile + 1, p_next);
-        p_now = p_next;
-        p_next = p_then;
-        if ((tile - tile0) % kFold == kFold - 1) fold();
-      }
-      if (!folded || (tile1 - tile0) % kFold != 0) fold();
-    }
-    __syncthreads();
-
-    // ---- the warps' sums, and the other blocks' where the segment is cut
-    const int32_t c0 = int32_t(seg0 / share), c1 = int32_t((seg0 + user.nu - 1) / share);
-    const bool whole = c0 == c1;
-    float* part = a.partial + (int64_t(blockIdx.x) * 2 + (tile0 == 0 ? 1 : 0)) * (S::kGroup * HD);
-    for (int i = tid; i < nq * HD; i += kWarps * 32) {
-      const int q = i / HD, c = i % HD;
-      float x = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-        for (int k = 0; k < S::kPieces; ++k) x += s_sum[w][q * S::kPieces + k][c];
-      if (tile0 == 0) {
-        const int64_t at = (row0 + q) * 4 * a.d + a.d + h * HD + c;
-        const float v = S::kF32 ? static_cast<const float*>(a.uvqk)[at]
-                                : __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at]);
-        x = fmaf(sh.self[q], v, x);
-      }
-      if (whole) a.av[(row0 + q) * a.d + h * HD + c] = x / float(a.n_norm);
-      else part[i] = x;
-    }
-    if (!whole) {
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int32_t k = atomicAdd(a.tickets + c0, 1);
-        sh.last = k == c1 - c0 ? 1 : 0;
-        if (sh.last) a.tickets[c0] = 0;            // as the next call expects it
-      }
-      __syncthreads();
-      if (sh.last) {
-        __threadfence();
-        for (int i = tid; i < nq * HD; i += kWarps * 32) {
-          float x = 0.f;
-          for (int32_t c = c0; c <= c1; ++c)
-            x += __ldcg(a.partial + (int64_t(c) * 2 + (c == c0 ? 1 : 0)) * (S::kGroup * HD) + i);
-          a.av[(row0 + i / HD) * a.d + h * HD + i % HD] = x / float(a.n_norm);
+          *p0 = x0;
+          *p1 = x1;
+          acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
         }
       }
+      ++folds;
+      chain = 0;
     }
-    __syncthreads();
-    u0 += tile1 - tile0;
+    if (end) {
+      const Part part = p;                         // the stage goes back before the join
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[st]);
+      if (!sync() || !finish<S, HD>(a, part, s_sum, ring.self, &ring.last, sync)) {
+        err |= HSTU_DEVERR_TIMEOUT;
+        break;
+      }
+    } else {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[st]);
+    }
   }
   if (err != 0) atomicOr(a.error, err);
+}
+
+// No more blocks than there can be units.
+template <class S>
+unsigned grid_of(const PagesArgs& a) {
+  const int64_t keys = (a.width << a.page_shift) / S::kUnit + 1;
+  const int64_t most = a.R < INT32_MAX / (a.H * keys) ? a.R * a.H * keys : INT32_MAX;
+  const int64_t grid = int64_t(a.num_sms) * S::kPerSm;
+  return unsigned(grid < most ? grid : most);
 }
 
 template <int FMT, int HD, int NT>
 cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
   using S = Shape<FMT, HD, NT>;
-  // no more blocks than there can be units
-  const int64_t keys = (a.width << a.page_shift) / S::kUnit + 1;
-  const int64_t most = (a.R < INT32_MAX / (a.H * keys) ? a.R * a.H * keys : INT32_MAX);
-  const int64_t grid = int64_t(a.num_sms) * S::kPerSm;
-  static_assert(S::kPerSm <= kPagesBlocksPerSm && S::kGroup * HD <= kPagesPartial, "workspace");
-  pages_attention_kernel<FMT, HD, NT>
-      <<<unsigned(grid < most ? grid : most), kWarps * 32, 0, st>>>(a);
+  static_assert(S::kPerSm <= kPagesBlocksPerSm, "workspace");
+  static_assert(S::kGroup * HD <= kPagesPartial && S::kGroup <= 8, "workspace");
+  static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kRows, "operand");
+  static_assert(S::kTimesAt >= S::kScalesAt && (S::kF32 || S::kStages * S::kStageBytes <= 128 * 1024), "ring");
+  if constexpr (S::kF32) {
+    pages_attention_f32_kernel<HD, NT><<<grid_of<S>(a), S::kThreads, 0, st>>>(a);
+  } else {
+    static std::atomic<uint64_t> done{0};
+    constexpr int bytes = S::kStages * S::kStageBytes;
+    const cudaError_t e = smem_opt_in(pages_attention_kernel<FMT, HD, NT>, bytes, done);
+    if (e != cudaSuccess) return e;
+    pages_attention_kernel<FMT, HD, NT><<<grid_of<S>(a), S::kThreads, bytes, st>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -465,3 +465,24 @@ def test_a_captured_call_follows_lengths_tables_and_streams():
         _check(av, pool, uvqk, [1, 1, 1], lens, ts, rp, rt, cfg)
     assert h.device_error() == 0
     h.close()
+
+
+@pytest.mark.parametrize("fmt,d,H", [("bf16", 256, 4), ("e4m3", 256, 2)])
+def test_an_expired_wait_is_reported_and_the_handle_recovers(fmt, d, H):
+    """With a bound of one cycle the pipeline gives up (the copies still land before the blocks
+    leave); with the default bound the same handle gives the result again."""
+    ps, lens, counts = 16, [900, 40, 0, 333], [1, 1, 1, 1]
+    h = _handle(d, H, fmt)
+    pool = _filled(h, d, H, fmt, ps, lens, seed=33)
+    uvqk, ts = _query(d, fmt, counts, seed=34)
+    rp, rt = _tables(128, 128, seed=35)
+    ref = _attend(h, pool, uvqk, counts, lens, ts, rp, rt)
+    assert h.device_error() == 0
+    hstu.hstu_set_wait_limit(h.h, 1)
+    _attend(h, pool, uvqk, counts, lens, ts, rp, rt)
+    assert h.device_error() & hstu.HSTU_DEVERR_TIMEOUT
+    hstu.hstu_set_wait_limit(h.h, 0)
+    for _ in range(2):
+        assert torch.equal(_attend(h, pool, uvqk, counts, lens, ts, rp, rt), ref)
+    assert h.device_error() == 0
+    h.close()
