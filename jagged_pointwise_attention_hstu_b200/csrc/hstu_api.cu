@@ -118,6 +118,19 @@ bool make_tmap_2d_f32_sw128(CUtensorMap* m, const void* base, uint64_t inner, ui
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_2d_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                           uint32_t box_outer) {
+  auto fn = encode_fn();
+  if (fn == nullptr || outer == 0 || inner == 0) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {128, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_1d_i64(CUtensorMap* m, const void* base, uint64_t n, uint32_t box) {
   auto fn = encode_fn();
   if (fn == nullptr || n == 0) return false;
@@ -1430,6 +1443,8 @@ hstu_status check_pool(const hstu_handle* h, const hstu_page_pool* p, bool need_
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)) != 0 ||
       p->num_pages < 1)
     return HSTU_ERR_INVALID_ARG;
+  if (int64_t(p->num_pages) * h->cfg.num_heads * 2 * p->page_size > INT32_MAX)
+    return HSTU_ERR_UNSUPPORTED;      // rows of the pool are 32-bit coordinates of its copies
   if (p->kv == nullptr || !hstu::aligned16(p->kv)) return HSTU_ERR_INVALID_ARG;
   if (p->format == HSTU_PAGES_E4M3 && (p->scales == nullptr || !hstu::aligned16(p->scales)))
     return HSTU_ERR_INVALID_ARG;

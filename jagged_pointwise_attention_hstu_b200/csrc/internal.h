@@ -370,6 +370,9 @@ bool make_tmap_2d_f32_sw128(CUtensorMap* m, const void* base, uint64_t inner, ui
 // bf16 [outer, inner] row-major, 64-byte swizzle (box_inner * 2 <= 64).
 bool make_tmap_2d_bf16_sw64(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// bytes [outer, inner] row-major, boxes of 128 bytes x box_outer rows, 128-byte swizzle.
+bool make_tmap_2d_u8_sw128(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                           uint32_t box_outer);
 bool make_tmap_1d_i64(CUtensorMap* m, const void* base, uint64_t n, uint32_t box);
 
 }  // namespace hstu

@@ -43,6 +43,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "pages.cuh"
@@ -108,10 +109,12 @@ struct Shape {
   static constexpr int kUnit = kWarps * kStep;                  // keys of a unit
   static constexpr int kPad = HD + 8;                           // row stride of the sums
   static constexpr int kThreads = 32 * (kWarps + (kF32 ? 0 : 1));
-  // the ring: a unit's keys and values, scales and times
-  static constexpr int kScalesAt = 2 * kUnit * kRow;
-  static constexpr int kTimesAt = kScalesAt + (kF16 ? 2 * kUnit : 0);
-  static constexpr int kStageBytes = kTimesAt + 8 * kUnit;
+  // the ring: the stages' keys and values, then their times and scales
+  static constexpr bool kSwizzle = !kF32 && kRow >= 128;        // rows of 128 bytes, TMA's swizzle
+  static constexpr int kHalves = kSwizzle ? kRow / 128 : 1;     // boxes of 128 bytes of a row
+  static constexpr int kDataBytes = 2 * kUnit * kRow;
+  static constexpr int kSideBytes = 8 * kUnit + (kF16 ? 2 * kUnit : 0);
+  static constexpr int kRingBytes(int stages) { return stages * (kDataBytes + kSideBytes); }
   static constexpr int kStages = kRow == 256 ? 2 : 3;
   static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT == 2 ? 2 : 3);
 };
@@ -282,36 +285,37 @@ __device__ __forceinline__ float bias_of(const PagesArgs& a, const int4* s_time,
   return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
 }
 
-// SiLU of each row's score with itself: a warp a row.
-template <class S, int HD>
-__device__ __forceinline__ void self_scores(const PagesArgs& a, const Part& p, float bias,
-                                            float* self, int& err) {
+// What each row adds of itself, SiLU(s_r) v_r: a warp a row.
+template <class S, int HD, class Self>
+__device__ __forceinline__ void self_terms(const PagesArgs& a, const Part& p, float bias,
+                                           Self& self, int& err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int q = warp; q < p.nq; q += kWarps) {
-    const int64_t at = (p.row0 + q) * 4 * a.d + 2 * a.d + p.h * HD + lane;
-    float s = 0.f;
+    const int64_t at = (p.row0 + q) * 4 * a.d + a.d + p.h * HD + lane;
+    auto load = [&](int64_t i) {
+      return S::kF32 ? static_cast<const float*>(a.uvqk)[i]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[i]);
+    };
+    float s = 0.f, v[HD / 32];
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e) {
-      if (S::kF32)
-        s = fmaf(static_cast<const float*>(a.uvqk)[at + 32 * e],
-                 static_cast<const float*>(a.uvqk)[at + a.d + 32 * e], s);
-      else
-        s = fmaf(__bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + 32 * e]),
-                 __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at + a.d + 32 * e]), s);
+      v[e] = load(at + 32 * e);
+      s = fmaf(load(at + a.d + 32 * e), load(at + 2 * a.d + 32 * e), s);
     }
-    s = warp_sum(s) + bias;
     const int64_t ts = __ldg(a.ts + p.row0 + q);
     if (ts < 0 || ts >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
-    if (lane == 0) self[q] = silu(s);
+    s = silu(warp_sum(s) + bias);
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e) self[q][lane + 32 * e] = s * v[e];
   }
 }
 
 // The warps' sums of a part, by the 128 threads that compute: written out, or
 // left for the last block of the segment, which joins the parts in block order.
 // sync() is a barrier of these threads; it returns false to give up.
-template <class S, int HD, class Sum, class Sync>
+template <class S, int HD, class Sum, class Self, class Sync>
 __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, const Sum& sum,
-                                       const float* self, int32_t* last, Sync sync) {
+                                       const Self& self, int32_t* last, Sync sync) {
   const int tid = threadIdx.x;
   const bool whole = p.c0 == p.c1;
   float* part = a.partial + (int64_t(blockIdx.x) * 2 + (p.tile0 == 0 ? 1 : 0)) * (S::kGroup * HD);
@@ -322,12 +326,7 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, const 
     for (int w = 0; w < kWarps; ++w)
 #pragma unroll
       for (int k = 0; k < S::kPieces; ++k) x += sum[w][q * S::kPieces + k][c];
-    if (p.tile0 == 0) {
-      const int64_t at = (p.row0 + q) * 4 * a.d + a.d + p.h * HD + c;
-      const float v = S::kF32 ? static_cast<const float*>(a.uvqk)[at]
-                              : __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[at]);
-      x = fmaf(self[q], v, x);
-    }
+    if (p.tile0 == 0) x += self[q][c];
     if (whole) a.av[(p.row0 + q) * a.d + p.h * HD + c] = x / float(a.n_norm);
     else part[i] = x;
   }
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   __shared__ Plan plan;
   __shared__ int4 s_time[128];
   __shared__ float s_sum[kWarps][NT][S::kPad];
-  __shared__ float s_self[8];
+  __shared__ float s_self[NT][HD];
   __shared__ int32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k4 = lane >> 3, t8 = lane & 7;
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   while (walk.next(a, p)) {
     const int32_t n = p.n;
     const int32_t* table = a.table + int64_t(p.b) * a.width;
-    if (p.tile0 == 0) self_scores<S, HD>(a, p, self_bias, s_self, err);
+    if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
     float q[NT][4 * E], o[NT][4 * E];
     int64_t now[NT];
 #pragma unroll
@@ -473,11 +472,10 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
 
 // One unit on its way through the ring.
 struct Unit {
+  int4 what;             // tile, runs (below) whose page index is none, Flag, cached rows
   Part part;
-  int32_t tile;
-  uint32_t bad;          // runs (below) whose page index is none
-  int32_t stop;
 };
+enum Flag { kFirst = 1, kLast = 2, kStop = 4 };   // of its part; no more units
 
 // untiled bulk copy global -> shared; all of dst, src and bytes multiples of 16
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -518,26 +516,30 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 
 template <class S>
 struct Ring {
-  uint64_t full[S::kStages], empty[S::kStages], turn;
+  uint64_t head[S::kStages], full[S::kStages], empty[S::kStages], turn;
   Unit unit[S::kStages];
   int32_t last;
-  float self[8];
 };
 
 // A unit's keys lie in runs of run = min(page_size, kUnit) keys, a page each:
 // [run][plane][key] in the stage, as in the pool; its scales [run][plane][key],
-// its times [key].
+// its times [key].  Rows of 64 bytes come as they are, by untiled copies.  The
+// rows of 128 and 256 bytes would meet in the same banks: they come through a
+// tensor map, [run][plane][half][key] of 128 bytes with TMA's swizzle (16-byte
+// chunk c of row r at c ^ (r & 7)), in boxes of a run or of 16 keys.
 template <int FMT, int HD, int NT>
 __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD, NT>::kPerSm))
-    pages_attention_kernel(const PagesArgs a) {
+    pages_attention_kernel(const PagesArgs a, const __grid_constant__ CUtensorMap map_run,
+                           const __grid_constant__ CUtensorMap map_16) {
   using S = Shape<FMT, HD, NT>;
   using namespace sm100;
   constexpr int NB = S::kBlocks;
-  extern __shared__ __align__(128) uint8_t stages[];
+  extern __shared__ __align__(1024) uint8_t stages[];
   __shared__ Plan plan;
   __shared__ Ring<S> ring;
   __shared__ int4 s_time[128];
   __shared__ float s_sum[kWarps][S::kRows][S::kPad];
+  __shared__ float s_self[S::kGroup][HD];
   // P of a warp's step, a row per column of the operand
   __shared__ __align__(16) uint16_t s_p[kWarps][S::kRows][S::kStep + 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -545,13 +547,13 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   int64_t u0, u1;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&ring.head[s], 1);
       mbar_init(&ring.full[s], 1);
       mbar_init(&ring.empty[s], kWarps);
     }
     mbar_init(&ring.turn, kWarps);
     fence_mbarrier_init();
   }
-  if (tid < 128) fill_time(a, s_time, tid);
   if (!make_plan<S>(a, plan, u0, u1)) return;
   const int32_t run_shift = (1 << a.page_shift) < S::kUnit ? a.page_shift : 31 - __clz(S::kUnit);
   const int32_t run = 1 << run_shift;
@@ -588,34 +590,46 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         const unsigned bad = __ballot_sync(0xffffffffu, page == -2);
         if (bad != 0) err |= HSTU_DEVERR_PAGES;
         if (lane == 0) {
-          Unit& u = ring.unit[s];
-          u.part = p;
-          u.tile = tile;
-          u.bad = bad;
-          u.stop = 0;
+          ring.unit[s].part = p;
+          ring.unit[s].what = make_int4(tile, int(bad), (tile == p.tile0 ? kFirst : 0) |
+                                        (tile + 1 == p.tile1 ? kLast : 0), p.n);
+          mbar_arrive(&ring.head[s]);
           mbar_arrive_expect_tx(&ring.full[s], bytes);
         }
         __syncwarp();
         if (keys > 0) {
           uint64_t* bar = &ring.full[s];
-          const uint32_t at = smem_u32(stages) + s * S::kStageBytes;
+          const uint32_t data = smem_u32(stages) + s * S::kDataBytes;
+          const uint32_t side = smem_u32(stages) + S::kStages * S::kDataBytes + s * S::kSideBytes;
           const int32_t slot = j & ((1 << a.page_shift) - 1);
           const int64_t block = (((int64_t(page) * a.H + p.h) * 2) << a.page_shift) + slot;
           const uint32_t first = lane << (run_shift + 1);       // of the stage's blocks
-          const char* kv = static_cast<const char*>(a.kv) + block * S::kRow;
-          const int64_t plane = int64_t(1) << a.page_shift;
-          bulk_load(at + S::kTimesAt + (lane << run_shift) * 8,
+          const int32_t plane = 1 << a.page_shift;
+          bulk_load(side + (lane << run_shift) * 8,
                     a.page_ts + (int64_t(page) << a.page_shift) + slot, keys * 8, bar);
-          if (keys == 1 << a.page_shift) {                      // a whole page: both planes at once
-            bulk_load(at + first * S::kRow, kv, 2 * keys * S::kRow, bar);
-            if (S::kF16) bulk_load(at + S::kScalesAt + first, a.scales + block, 2 * keys, bar);
+          const bool both = keys == plane;                      // a whole page: planes at once
+          if constexpr (S::kSwizzle) {
+            const int32_t y = int32_t(block), step = keys == run ? run : 16;
+            const CUtensorMap* map = keys == run ? &map_run : &map_16;
+            uint8_t* to = stages + s * S::kDataBytes + first * S::kRow;
+            for (int32_t r = 0; r < keys; r += step)
+#pragma unroll
+              for (int x = 0; x < S::kHalves; ++x) {
+                tma_load_2d(to + (x * run + r) * 128, map, bar, 128 * x, y + r);
+                tma_load_2d(to + (x * run + r) * 128 + run * S::kRow, map, bar, 128 * x,
+                            y + plane + r);
+              }
           } else {
-            bulk_load(at + first * S::kRow, kv, keys * S::kRow, bar);
-            bulk_load(at + (first + run) * S::kRow, kv + plane * S::kRow, keys * S::kRow, bar);
-            if (S::kF16) {
-              bulk_load(at + S::kScalesAt + first, a.scales + block, keys, bar);
-              bulk_load(at + S::kScalesAt + first + run, a.scales + block + plane, keys, bar);
-            }
+            const char* kv = static_cast<const char*>(a.kv) + block * S::kRow;
+            bulk_load(data + first * S::kRow, kv, (both ? 2 : 1) * keys * S::kRow, bar);
+            if (!both)
+              bulk_load(data + (first + run) * S::kRow, kv + int64_t(plane) * S::kRow,
+                        keys * S::kRow, bar);
+          }
+          if constexpr (S::kF16) {
+            const uint32_t at = side + 8 * S::kUnit + first;
+            bulk_load(at, a.scales + block, (both ? 2 : 1) * keys, bar);
+            if (!both) bulk_load(at + run, a.scales + block + plane, keys, bar);
           }
         }
         ++issued;
@@ -624,14 +638,13 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     const int s = issued % S::kStages;
     if (ok) ok = wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
     if (ok && lane == 0) {
-      ring.unit[s].stop = 1;
-      mbar_arrive(&ring.full[s]);
+      ring.unit[s].what = make_int4(0, 0, kStop, 0);
+      mbar_arrive(&ring.head[s]);
     }
     if (!ok) err |= HSTU_DEVERR_TIMEOUT;
     // no copy may land after the block has gone, whoever gave up
     for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0; k < issued; ++k)
-      if (k % S::kStages != s || !ok)
-        mbar_wait(&ring.full[k % S::kStages], (k / S::kStages) & 1);
+      mbar_wait(&ring.full[k % S::kStages], (k / S::kStages) & 1);
     if (err != 0) atomicOr(a.error, err);
     return;
   }
@@ -655,28 +668,35 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     turn ^= 1;
     return __all_sync(0xffffffffu, ok) != 0;
   };
+  // the 16-byte chunks of a key that are the lane's, and which of its rows a lane's key is
+  auto chunk = [&](int y) { return S::kSwizzle ? 2 * t + (y & 1) + 8 * (y >> 1) : t; };
+  auto key_of = [&](int i) { return S::kSwizzle ? 2 * t + (i & 1) + 8 * (i >> 1) : t + 4 * i; };
+  const int spot = (lane & 16) + (S::kSwizzle ? 4 * (lane >> 1 & 3) + (lane & 1) + 2 * (lane >> 3 & 1)
+                                              : 4 * (lane & 3) + (lane >> 2 & 3));
   uint32_t qb[QT][KS][2];
   float q_scale[QT], inv[NT], acc[MT][NT][4];
-  int64_t now0 = 0;
-  int folds = 0, chain = 0;
+  int64_t row0 = 0, now0 = 0;
+  int nq = 1, folds = 0, chain = 0;
+  fill_time(a, s_time, tid);
+  bool up = sync(), done = false;
 
-  for (uint32_t k = 0;; ++k) {
+  for (uint32_t k = 0; up; ++k) {
     const int st = k % S::kStages;
-    const bool here = wait_for(&ring.full[st], (k / S::kStages) & 1, limit);
-    if (!__all_sync(0xffffffffu, here)) {
-      err |= HSTU_DEVERR_TIMEOUT;
+    const uint32_t parity = (k / S::kStages) & 1;
+    if (!__all_sync(0xffffffffu, wait_for(&ring.head[st], parity, limit))) break;
+    const int4 what = ring.unit[st].what;
+    if (what.z & kStop) {
+      done = true;
       break;
     }
-    const Unit& unit = ring.unit[st];
-    if (unit.stop) break;
-    const Part& p = unit.part;
-    const int32_t n = p.n, nq = p.nq, tile = unit.tile;
-    const bool end = tile + 1 == p.tile1;
+    const int32_t tile = what.x, n = what.w;
 
-    if (tile == p.tile0) {
-      // ---- a new part: q, and nothing summed
-      if (p.tile0 == 0) self_scores<S, HD>(a, p, self_bias, ring.self, err);
-      now0 = __ldg(a.ts + p.row0);
+    if (what.z & kFirst) {
+      // ---- a new part: q, and nothing summed; its pages are on their way
+      const Part& p = ring.unit[st].part;
+      nq = p.nq;
+      row0 = p.row0;
+      now0 = __ldg(a.ts + row0);
       // Columns 2i and 2i + 1 of the score product are query i, with the even and the odd
       // pairs of its dimensions: what the lane's g is, at its t's dimensions.
 #pragma unroll
@@ -684,12 +704,12 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         const int q = 4 * i + (g >> 1) < nq ? 4 * i + (g >> 1) : nq - 1;
         const bool odd = (g & 1) != 0;
         const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.uvqk) + (p.row0 + q) * 4 * a.d + 2 * a.d + p.h * HD);
+            static_cast<const __nv_bfloat16*>(a.uvqk) + (row0 + q) * 4 * a.d + 2 * a.d + p.h * HD);
         q_scale[i] = 1.f;
         if constexpr (!S::kF16) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
-            const uint4 v = __ldg(src + t + 4 * c);
+            const uint4 v = __ldg(src + chunk(c));
             qb[i][c][0] = odd ? v.y : v.x;
             qb[i][c][1] = odd ? v.w : v.z;
           }
@@ -700,8 +720,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           float m = 0.f;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
-            unpack_bf16(__ldg(src + 2 * (t + 4 * c)), x[c]);
-            unpack_bf16(__ldg(src + 2 * (t + 4 * c) + 1), x[c] + 8);
+            unpack_bf16(__ldg(src + 2 * chunk(c)), x[c]);
+            unpack_bf16(__ldg(src + 2 * chunk(c) + 1), x[c] + 8);
 #pragma unroll
             for (int y = 0; y < 16; ++y) m = fmaxf(m, fabsf(x[c][y]));
           }
@@ -735,30 +755,32 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
 #pragma unroll
       for (int i = 0; i < NT; ++i) inv[i] = __int_as_float((127 + 126) << 23);
       folds = chain = 0;
+      if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
     }
+    if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], parity, limit))) break;
 
     const int32_t k0 = warp * S::kStep, j0 = tile * S::kUnit + k0;   // the warp's keys
     if (j0 < n) {
-      const uint32_t base = smem_u32(stages) + st * S::kStageBytes;
-      // the lane's own key
+      const uint32_t data = smem_u32(stages) + st * S::kDataBytes;
+      // the lane's own key; scales are [run][plane][key]
       const int32_t kl = k0 + (lane & (S::kStep - 1)), jl = tile * S::kUnit + kl;
-      const bool mine = jl < n && !(unit.bad >> (kl >> run_shift) & 1);
-      const uint2 tw = lds8(base + S::kTimesAt + kl * 8);
-      const int64_t then = int64_t(uint64_t(tw.y) << 32 | tw.x);
+      const bool mine = jl < n && !(uint32_t(what.y) >> (kl >> run_shift) & 1);
+      const uint8_t* side = stages + S::kStages * S::kDataBytes + st * S::kSideBytes;
+      const int64_t then = *reinterpret_cast<const int64_t*>(side + 8 * kl);
       float ks = 1.f, vs = 1.f;
-      // [run][plane][key]
-      const uint32_t own = ((kl >> run_shift) << (run_shift + 1)) + (kl & (run - 1));
       if constexpr (S::kF16) {
-        const uint8_t* sc = stages + st * S::kStageBytes + S::kScalesAt + own;
+        const uint8_t* sc = side + 8 * S::kUnit + ((kl >> run_shift) << (run_shift + 1)) + (kl & (run - 1));
         ks = block_scale(sc[0]);
         vs = block_scale(sc[run]);
       }
       float s[NB][2][QT];                // of key 16 nb + 8 x + g and row 4i + t
-      uint32_t at[NB];                   // the blocks' first keys
+      uint32_t at[NB];                   // the blocks' runs of keys
+      int32_t key0[NB];                  // and their first keys there
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int32_t kb = k0 + 16 * nb;
-        at[nb] = base + (((kb >> run_shift) << (run_shift + 1)) + (kb & (run - 1))) * S::kRow;
+        at[nb] = data + ((kb >> run_shift) << (run_shift + 1)) * S::kRow;
+        key0[nb] = kb & (run - 1);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float c[QT][4];
@@ -766,7 +788,10 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           for (int i = 0; i < QT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 #pragma unroll
           for (int y = 0; y < KC; ++y) {
-            const uint4 v = lds16(at[nb] + (8 * x + g) * S::kRow + 64 * y + 16 * t);
+            const uint32_t r = key0[nb] + 8 * x + g, c16 = chunk(y);
+            const uint4 v = lds16(S::kSwizzle ? at[nb] + ((c16 >> 3) * run + r) * 128 +
+                                                    (((c16 & 7) ^ g) << 4)
+                                              : at[nb] + r * S::kRow + 16 * c16);
             if constexpr (S::kF16) {
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -788,85 +813,110 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           for (int i = 0; i < QT; ++i) s[nb][x][i] = c[i][0] + c[i][3];
         }
       }
-      // Key (lane & 15) of its block is row (key >> 2) of the lane (key & 3)'s four keys
-      const int spot = (lane & 16) + 4 * (lane & 3) + (lane >> 2 & 3);
-      __syncwarp();                      // the last step's P has been read
+      // ---- a lane a key: N rows of q at once, from row 4i on (those behind nq are copies of
+      // the last, in columns that nobody reads)
+      auto score = [&](auto count, int i) {
+        constexpr int N = decltype(count)::value;
+        float y[N];
 #pragma unroll
-      for (int i = 0; i < QT; ++i) {
-        for (int q = 4 * i; q < nq && q < 4 * i + 4; ++q) {   // a lane a key
-          const int src = 4 * (lane & 7) + (q & 3);
+        for (int c = 0; c < N; ++c) {
+          const int src = 4 * (lane & 7) + c;
           const float y0 = __shfl_sync(0xffffffffu, s[0][0][i], src);
           const float y1 = __shfl_sync(0xffffffffu, s[0][1][i], src);
-          float y = lane & 8 ? y1 : y0;
+          y[c] = lane & 8 ? y1 : y0;
           if constexpr (NB == 2) {
             const float y2 = __shfl_sync(0xffffffffu, s[1][0][i], src);
             const float y3 = __shfl_sync(0xffffffffu, s[1][1][i], src);
             const float z = lane & 8 ? y3 : y2;
-            y = lane & 16 ? z : y;
+            y[c] = lane & 16 ? z : y[c];
           }
-          if constexpr (S::kF16) y = y * __shfl_sync(0xffffffffu, q_scale[i], 8 * (q & 3)) * ks;
-          const int64_t now = q == 0 ? now0 : __ldg(a.ts + p.row0 + q);
-          y = silu(y + bias_of(a, s_time, pos_far, n, jl, now, then));
-          if constexpr (S::kF16) y *= vs;
-          y = mine ? y : 0.f;            // no key here: what memory holds must not reach the sum
-          if constexpr (S::kF16) {
-            // e4m3: four rows a tile of scores, and a tile of P
-            float f = __shfl_sync(0xffffffffu, inv[i], q & 3);
-            if (__any_sync(0xffffffffu, fabsf(y) * f > 32768.f)) {   // raise the row's power
-              float m = fabsf(y);
+          if constexpr (S::kF16) y[c] = y[c] * __shfl_sync(0xffffffffu, q_scale[i], 8 * c) * ks;
+          int64_t now = now0;
+          if (4 * i + c > 0) now = __ldg(a.ts + row0 + (4 * i + c < nq ? 4 * i + c : nq - 1));
+          y[c] = silu(y[c] + bias_of(a, s_time, pos_far, n, jl, now, then));
+          if constexpr (S::kF16) y[c] *= vs;
+          y[c] = mine ? y[c] : 0.f;      // no key here: what memory holds must not reach the sum
+        }
+        if constexpr (S::kF16) {         // four rows a tile of scores, and a tile of P
+          float f[N];
+          bool over = false;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            f[c] = __shfl_sync(0xffffffffu, inv[i], c);
+            over |= fabsf(y[c]) * f[c] > 32768.f;
+          }
+          if (__any_sync(0xffffffffu, over)) {                       // raise a row's power
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              float m = fabsf(y[c]);
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              if (!(m * f[c] > 32768.f)) continue;
               int e = int(__float_as_uint(m) >> 23) - 127 - 6;       // to [2^6, 2^7): room to grow
               e = e > 126 ? 126 : (e < -126 ? -126 : e);
               const float f1 = __int_as_float((127 - e) << 23);
-              const float ratio = t == (q & 3) ? f1 / f : 1.f;
-              if (t == (q & 3)) inv[i] = f1;
-              f = f1;
+              const float ratio = t == c ? f1 / f[c] : 1.f;
+              if (t == c) inv[i] = f1;
+              f[c] = f1;
 #pragma unroll
               for (int m2 = 0; m2 < MT; ++m2) {
                 acc[m2][i][0] *= ratio, acc[m2][i][1] *= ratio;
                 acc[m2][i][2] *= ratio, acc[m2][i][3] *= ratio;
               }
             }
-            y *= f;
-            const __half hi = __float2half_rn(y);
-            const __half lo = __float2half_rn(y - __half2float(hi));
+          }
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            y[c] *= f[c];
+            const __half hi = __float2half_rn(y[c]);
+            const __half lo = __float2half_rn(y[c] - __half2float(hi));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[2 * q][spot] = __half_as_ushort(hi);
-              ps[2 * q + 1][spot] = __half_as_ushort(lo);
+              ps[8 * i + 2 * c][spot] = __half_as_ushort(hi);
+              ps[8 * i + 2 * c + 1][spot] = __half_as_ushort(lo);
             }
-          } else {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(y);
-            y -= __bfloat162float(hi);
-            const __nv_bfloat16 mid = __float2bfloat16_rn(y);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(y - __bfloat162float(mid));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(y[c]);
+            y[c] -= __bfloat162float(hi);
+            const __nv_bfloat16 mid = __float2bfloat16_rn(y[c]);
+            const __nv_bfloat16 lo = __float2bfloat16_rn(y[c] - __bfloat162float(mid));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[3 * q][spot] = __bfloat16_as_ushort(hi);
-              ps[3 * q + 1][spot] = __bfloat16_as_ushort(mid);
-              ps[3 * q + 2][spot] = __bfloat16_as_ushort(lo);
+              ps[3 * c][spot] = __bfloat16_as_ushort(hi);
+              ps[3 * c + 1][spot] = __bfloat16_as_ushort(mid);
+              ps[3 * c + 2][spot] = __bfloat16_as_ushort(lo);
             }
           }
         }
+      };
+      __syncwarp();                      // the last step's P has been read
+#pragma unroll
+      for (int i = 0; i < QT; ++i) {
+        if (nq == 4 * i + 1) score(std::integral_constant<int, 1>{}, i);
+        else if (nq > 4 * i) score(std::integral_constant<int, (S::kGroup < 4 ? S::kGroup : 4)>{}, i);
       }
       __syncwarp();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         if (j0 + 16 * nb >= n) continue;           // nothing was loaded there
-        uint2 pb[NT];                  // P of the keys t, t + 4, t + 8, t + 12, column g
+        uint2 pb[NT];                  // P of the lane's four keys, column g
 #pragma unroll
         for (int i = 0; i < NT; ++i)
           pb[i] = *reinterpret_cast<const uint2*>(&ps[8 * i + g][16 * nb + 4 * t]);
         uint32_t v[4][VW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t row = at[nb] + (run + t + 4 * i) * S::kRow + (VW == 2 ? 8 : 16) * g;
+          const uint32_t r = key0[nb] + key_of(i);
+          const uint32_t row = at[nb] + run * S::kRow +
+                               (S::kSwizzle ? r * 128 + ((g ^ (r & 7)) << 4) : r * S::kRow + 8 * g);
           if constexpr (VW == 2) {
             const uint2 x = lds8(row);
             v[i][0] = x.x, v[i][1] = x.y;
           } else {
 #pragma unroll
             for (int c = 0; c < VW / 4; ++c) {
-              const uint4 x = lds16(row + 128 * c);
+              const uint4 x = lds16(row + 128 * run * c);
               v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
             }
           }
@@ -874,7 +924,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         if (j0 + 16 * nb + 16 > n) {               // rows behind the history: 0 * NaN
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (j0 + 16 * nb + t + 4 * i >= n)
+            if (j0 + 16 * nb + key_of(i) >= n)
 #pragma unroll
               for (int w = 0; w < VW; ++w) v[i][w] = 0u;
         }
@@ -899,7 +949,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     }
     // ---- the chain of products into the warp's fp32 sums
     ++chain;
-    if (chain == kFold || end) {
+    if (chain == kFold || (what.z & kLast)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
@@ -923,19 +973,17 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       ++folds;
       chain = 0;
     }
-    if (end) {
-      const Part part = p;                         // the stage goes back before the join
+    if (what.z & kLast) {
+      const Part part = ring.unit[st].part;        // the stage goes back before the join
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);
-      if (!sync() || !finish<S, HD>(a, part, s_sum, ring.self, &ring.last, sync)) {
-        err |= HSTU_DEVERR_TIMEOUT;
-        break;
-      }
+      up = sync() && finish<S, HD>(a, part, s_sum, s_self, &ring.last, sync);
     } else {
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);
     }
   }
+  if (!done) err |= HSTU_DEVERR_TIMEOUT;
   if (err != 0) atomicOr(a.error, err);
 }
 
@@ -954,15 +1002,26 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
   static_assert(S::kPerSm <= kPagesBlocksPerSm, "workspace");
   static_assert(S::kGroup * HD <= kPagesPartial && S::kGroup <= 8, "workspace");
   static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kRows, "operand");
-  static_assert(S::kTimesAt >= S::kScalesAt && (S::kF32 || S::kStages * S::kStageBytes <= 128 * 1024), "ring");
+  static_assert(S::kHalves * 128 >= S::kRow || !S::kSwizzle, "boxes");
+  static_assert(S::kF32 || S::kRingBytes(S::kStages) <= 128 * 1024, "ring");
   if constexpr (S::kF32) {
     pages_attention_f32_kernel<HD, NT><<<grid_of<S>(a), S::kThreads, 0, st>>>(a);
   } else {
     static std::atomic<uint64_t> done{0};
-    constexpr int bytes = S::kStages * S::kStageBytes;
-    const cudaError_t e = smem_opt_in(pages_attention_kernel<FMT, HD, NT>, bytes, done);
+    constexpr int bytes = S::kRingBytes(S::kStages);
+    cudaError_t e = smem_opt_in(pages_attention_kernel<FMT, HD, NT>, bytes, done);
     if (e != cudaSuccess) return e;
-    pages_attention_kernel<FMT, HD, NT><<<grid_of<S>(a), S::kThreads, bytes, st>>>(a);
+    CUtensorMap run, block;
+    memset(&run, 0, sizeof(run));
+    memset(&block, 0, sizeof(block));
+    if (S::kSwizzle) {
+      const int page = 1 << a.page_shift;
+      const uint64_t rows = uint64_t(a.num_pages) * a.H * 2 * page;
+      if (!make_tmap_2d_u8_sw128(&run, a.kv, S::kRow, rows, page < S::kUnit ? page : S::kUnit) ||
+          !make_tmap_2d_u8_sw128(&block, a.kv, S::kRow, rows, 16))
+        return cudaErrorInvalidValue;
+    }
+    pages_attention_kernel<FMT, HD, NT><<<grid_of<S>(a), S::kThreads, bytes, st>>>(a, run, block);
   }
   return cudaGetLastError();
 }
