@@ -84,12 +84,13 @@ __device__ __forceinline__ Place place_of(const PagesArgs& a, int64_t r, int lan
     p.err = HSTU_DEVERR_PAGES;
     return p;
   }
+  // a length is an int32, and the rows of a user fewer than 2^30: no overflow past int64
   const int64_t pos = (a.lengths != nullptr ? int64_t(__ldg(a.lengths + b)) : 0) + (r - r0);
   if (pos < 0 || (pos >> a.page_shift) >= a.width) {
     p.err = HSTU_DEVERR_PAGES;
     return p;
   }
-  const int32_t page = __ldg(a.table + int64_t(b) * a.width + (pos >> a.page_shift));
+  const int32_t page = __ldg(a.table + (int64_t(b) * a.width + (pos >> a.page_shift)));
   if (page < 0 || page >= a.num_pages) {
     p.err = HSTU_DEVERR_PAGES;
     return p;
@@ -101,143 +102,231 @@ __device__ __forceinline__ Place place_of(const PagesArgs& a, int64_t r, int lan
   return p;
 }
 
-// Quantises eight values of one block whose finite maximum is m; 2^-e exact.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float m, int& e) {
-  e = block_exponent(m);
-  const float inv = __int_as_float((127 - e) << 23);
-  const float top = e == kMaxExponent ? 240.f : 448.f;
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float u = x[2 * i] * inv, v = x[2 * i + 1] * inv;
-    // fminf and fmaxf drop a NaN: a non-finite value is put back as NaN
-    u = fabsf(x[2 * i]) < INFINITY ? fminf(fmaxf(u, -top), top) : NAN;
-    v = fabsf(x[2 * i + 1]) < INFINITY ? fminf(fmaxf(v, -top), top) : NAN;
-    c[i] = __nv_cvt_float2_to_fp8x2(make_float2(u, v), __NV_SATFINITE, __NV_E4M3);
-  }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+// Four codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t four_codes(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
 }
 
-// One warp per row: the row's keys and values in chunks of 16 bytes, a lane a
-// chunk, straight into the row's blocks.  Bound by memory: a row reads
-// 2d elements and writes them (or their codes) once.
-template <int FMT>
+constexpr uint32_t kAbs = 0x7fff7fffu;
+// Two maxima of bf16; a NaN stays one.
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Codes of a lane's eight bf16 of a block that kLanes neighbouring lanes hold,
+// and the block's scale byte; by the whole warp.
+//
+// The maximum is taken of two bf16 at a time, and nothing is clamped, since
+// |x| <= 448 * 2^e by the choice of e.  Values that are not finite, and the
+// exponent that is held at 120, sit above 448 * 2^119 = bits 0x7F60: a warp
+// that has one takes the long way.
+template <int kLanes>
+__device__ __forceinline__ uint2 quantise8(const uint4& v, int& scale) {
+  uint32_t top = max2(max2(v.x & kAbs, v.y & kAbs), max2(v.z & kAbs, v.w & kAbs));
+#pragma unroll
+  for (int o = kLanes >> 1; o > 0; o >>= 1) top = max2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = max(top & 0xffffu, top >> 16);
+  float x[8];
+  unpack_bf16(v, x);
+  uint2 c;
+  if (!__any_sync(0xffffffffu, top > 0x7F60u)) {
+    // e + 127 with e = k - 8 for top in (1.75 * 2^(k - 1), 1.75 * 2^k]: 0x1F carries above it
+    scale = max(int((top + 0x1Fu) >> 7) - 8, kMinExponent + 127);
+    scale = top == 0 ? 127 : scale;
+    const float inv = __int_as_float((254 - scale) << 23);
+    c.x = four_codes(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    c.y = four_codes(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+  } else {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+#pragma unroll
+    for (int o = kLanes >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = block_exponent(m);
+    const float inv = __int_as_float((127 - e) << 23), most = e == kMaxExponent ? 240.f : 448.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)   // fminf and fmaxf would drop a NaN
+      x[i] = fabsf(x[i]) < INFINITY ? fminf(fmaxf(x[i] * inv, -most), most) : NAN;
+    c.x = four_codes(x[0], x[1], x[2], x[3]);
+    c.y = four_codes(x[4], x[5], x[6], x[7]);
+    scale = e + 127;
+  }
+  return c;
+}
+
+// A row's keys and values in chunks of 16 bytes, heads of the keys first: lane
+// `lane` has the chunks lane, lane + 32, ..., which are the same place of a
+// block's kPerHead whatever the block (96, fp32 only: heads of 24 chunks).
+template <int FMT, int HD>
+struct Chunks {
+  static constexpr int kElems = FMT == HSTU_PAGES_FP32 ? 4 : 8;   // elements of a chunk
+  static constexpr int kPerHead = HD / kElems;
+  static constexpr int kBatch = 8;                                // of a lane, loaded at once
+  int lane, H, shift;
+  __device__ __forceinline__ Chunks(const PagesArgs& a)
+      : lane(threadIdx.x & 31), H(a.H), shift(a.page_shift) {}
+  __device__ __forceinline__ int all() const { return 2 * H * kPerHead; }
+  // of U | V | Q | K: K (the first half), then V
+  __device__ __forceinline__ int column(int c) const { return c + (c < H * kPerHead ? 3 * H * kPerHead : 0); }
+  __device__ __forceinline__ int in(int c) const {
+    return 32 % kPerHead == 0 ? lane % kPerHead : c % kPerHead;
+  }
+  // of the block, from the row's first: head h's keys are block 2h, its values 2h + 1
+  __device__ __forceinline__ int block(int c) const {
+    const int b = c / kPerHead;
+    return (2 * b - (b < H ? 0 : 2 * H - 1)) << shift;
+  }
+};
+
+// One warp per row, a lane a chunk, straight into the row's blocks.  Bound by
+// memory: a row reads 2d elements and writes them (or their codes) once.  All
+// of a lane's loads (d 1024: 8) are on their way before the row's place is
+// looked up.  What it took to get there were fewer instructions, about 75 a
+// chunk of e4m3 (65536 rows of d 1024: 137 us at 205).
+template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const PagesArgs a) {
-  constexpr int kElems = FMT == HSTU_PAGES_FP32 ? 4 : 8;   // elements of a chunk
+  using C = Chunks<FMT, HD>;
   check_offsets(a);
-  const int lane = threadIdx.x & 31;
   const int64_t r = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (r >= a.R) return;
-  const Place p = place_of(a, r, lane);
+  const C ch(a);
+  const int all = ch.all();
+  const uint4* src = static_cast<const uint4*>(a.uvqk) + r * (2 * all);
+  uint4 v[C::kBatch];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < C::kBatch; ++i) {
+      const int c = c0 + 32 * i + ch.lane;
+      v[i] = c < all ? __ldg(src + ch.column(c)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load(0);
+  const Place p = place_of(a, r, ch.lane);
   if (!p.ok) {
-    if (p.err != 0 && lane == 0) atomicOr(a.error, p.err);
+    if (p.err != 0 && ch.lane == 0) atomicOr(a.error, p.err);
     return;
   }
-  const uint4* src = static_cast<const uint4*>(a.uvqk) + r * (4 * a.d / kElems);
-  const int per_plane = a.d / kElems, per_head = a.hd / kElems;
-  const int chunks = 2 * per_plane;
-  if (lane == 0 && a.ts != nullptr) {
+  if (ch.lane == 0 && a.ts != nullptr) {
     const int64_t t = a.ts[r];
     if (t < 0 || t >= kMaxTimestamp) atomicOr(a.error, HSTU_DEVERR_TIMESTAMPS);
     a.page_ts[p.ts] = t;
   }
-  for (int c0 = 0; c0 < chunks; c0 += 32) {
-    const int c = c0 + lane;
-    const bool on = c < chunks;
-    const int plane = c >= per_plane ? 1 : 0;
-    const int k = c - plane * per_plane;              // chunk of the plane
-    const int h = on ? k / per_head : 0;
-    const int64_t block = p.row + ((int64_t(2 * h + plane)) << a.page_shift);
-    // input columns: U | V | Q | K
-    const uint4 v = on ? __ldg(src + (plane == 0 ? 3 : 1) * per_plane + k)
-                       : make_uint4(0u, 0u, 0u, 0u);
-    if (FMT != HSTU_PAGES_E4M3) {
-      if (on) static_cast<uint4*>(a.kv)[block * per_head + (k - h * per_head)] = v;
-    } else {
-      float x[8];
-      unpack_bf16(v, x);
-      float m = 0.f;
+  uint4* to = static_cast<uint4*>(a.kv) + p.row * C::kPerHead;
+  uint2* codes = static_cast<uint2*>(a.kv) + p.row * C::kPerHead;
+  uint8_t* scales = a.scales + p.row;
+  for (int c0 = 0;;) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-      // the lanes of one block are neighbours: 8 (head dim 64) or 16 (128)
-      for (int o = per_head >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      int e;
-      const uint2 q = quantise8(x, m, e);
-      if (on) {
-        static_cast<uint2*>(a.kv)[block * per_head + (k - h * per_head)] = q;
-        if (k == h * per_head) a.scales[block] = uint8_t(e + 127);
+    for (int i = 0; i < C::kBatch; ++i) {
+      if (c0 + 32 * i >= all) break;
+      const int c = c0 + 32 * i + ch.lane;
+      const int block = ch.block(c), in = ch.in(c);
+      if constexpr (FMT != HSTU_PAGES_E4M3) {
+        if (c < all) to[block * C::kPerHead + in] = v[i];
+      } else {
+        int scale;
+        const uint2 q = quantise8<C::kPerHead>(v[i], scale);
+        if (c < all) {
+          codes[block * C::kPerHead + in] = q;
+          if (in == 0) scales[block] = uint8_t(scale);
+        }
       }
     }
+    c0 += 32 * C::kBatch;
+    if (c0 >= all) break;
+    load(c0);
   }
 }
 
 // The way back: a warp per row, pages into the K and V columns of U|V|Q|K.
-template <int FMT>
+template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesArgs a) {
-  constexpr int kElems = FMT == HSTU_PAGES_FP32 ? 4 : 8;
+  using C = Chunks<FMT, HD>;
   check_offsets(a);
-  const int lane = threadIdx.x & 31;
   const int64_t r = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
   if (r >= a.R) return;
-  const Place p = place_of(a, r, lane);
+  const C ch(a);
+  const int all = ch.all();
+  const Place p = place_of(a, r, ch.lane);
   if (!p.ok) {
-    if (p.err != 0 && lane == 0) atomicOr(a.error, p.err);
+    if (p.err != 0 && ch.lane == 0) atomicOr(a.error, p.err);
     return;
   }
-  uint4* dst = static_cast<uint4*>(a.out) + r * (4 * a.d / kElems);
-  const int per_plane = a.d / kElems, per_head = a.hd / kElems;
-  const int chunks = 2 * per_plane;
-  if (lane == 0 && a.ts_out != nullptr) a.ts_out[r] = a.page_ts[p.ts];
-  for (int c = lane; c < chunks; c += 32) {
-    const int plane = c >= per_plane ? 1 : 0;
-    const int k = c - plane * per_plane;
-    const int h = k / per_head;
-    const int64_t block = p.row + ((int64_t(2 * h + plane)) << a.page_shift);
-    uint4 v;
-    if (FMT != HSTU_PAGES_E4M3) {
-      v = __ldg(static_cast<const uint4*>(a.kv) + block * per_head + (k - h * per_head));
-    } else {
-      const uint2 q = __ldg(static_cast<const uint2*>(a.kv) + block * per_head + (k - h * per_head));
-      const float s = block_scale(__ldg(a.scales + block));
-      float x[8];
-      unpack_e4m3(q.x, x);
-      unpack_e4m3(q.y, x + 4);
-      uint32_t w[4];
+  uint4* dst = static_cast<uint4*>(a.out) + r * (2 * all);
+  const uint4* from = static_cast<const uint4*>(a.kv) + p.row * C::kPerHead;
+  const uint2* codes = static_cast<const uint2*>(a.kv) + p.row * C::kPerHead;
+  const uint8_t* scales = a.scales + p.row;
+  if (ch.lane == 0 && a.ts_out != nullptr) a.ts_out[r] = a.page_ts[p.ts];
+  for (int c0 = ch.lane; c0 < all; c0 += 32 * C::kBatch) {
+    uint4 v[C::kBatch];
+    float s[C::kBatch];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {   // exact: 4 significant bits
-        const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i] * s, x[2 * i + 1] * s);
-        w[i] = *reinterpret_cast<const uint32_t*>(&t);
+    for (int i = 0; i < C::kBatch; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= all) continue;
+      const int block = ch.block(c), at = block * C::kPerHead + ch.in(c);
+      if constexpr (FMT != HSTU_PAGES_E4M3) {
+        v[i] = __ldg(from + at);
+      } else {
+        const uint2 q = __ldg(codes + at);
+        v[i].x = q.x;
+        v[i].y = q.y;
+        s[i] = block_scale(__ldg(scales + block));
       }
-      v = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    dst[(plane == 0 ? 3 : 1) * per_plane + k] = v;
+#pragma unroll
+    for (int i = 0; i < C::kBatch; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= all) continue;
+      if constexpr (FMT == HSTU_PAGES_E4M3) {
+        float x[8];
+        unpack_e4m3(v[i].x, x);
+        unpack_e4m3(v[i].y, x + 4);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // exact: 4 significant bits
+          const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * e] * s[i], x[2 * e + 1] * s[i]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      dst[ch.column(c)] = v[i];
+    }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_pages_write(const PagesArgs& a, cudaStream_t st) {
-  if (a.R <= 0 || a.B <= 0) return cudaSuccess;
-  const unsigned blocks = unsigned((a.R + kRowWarps - 1) / kRowWarps);
-  switch (a.format) {
-    case HSTU_PAGES_BF16: pages_write_kernel<HSTU_PAGES_BF16><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    case HSTU_PAGES_FP32: pages_write_kernel<HSTU_PAGES_FP32><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    case HSTU_PAGES_E4M3: pages_write_kernel<HSTU_PAGES_E4M3><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
+#define HSTU_PAGES_ROWS(KERNEL, F, D) \
+  KERNEL<F, D><<<blocks, kRowWarps * 32, 0, st>>>(a); \
+  return cudaGetLastError()
+#define HSTU_PAGES_DISPATCH(KERNEL)                                                 \
+  if (a.R <= 0 || a.B <= 0) return cudaSuccess;                                     \
+  const unsigned blocks = unsigned((a.R + kRowWarps - 1) / kRowWarps);              \
+  switch (a.format * 256 + a.hd) {                                                  \
+    case HSTU_PAGES_BF16 * 256 + 64: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_BF16, 64);   \
+    case HSTU_PAGES_BF16 * 256 + 128: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_BF16, 128); \
+    case HSTU_PAGES_E4M3 * 256 + 64: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_E4M3, 64);   \
+    case HSTU_PAGES_E4M3 * 256 + 128: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_E4M3, 128); \
+    case HSTU_PAGES_FP32 * 256 + 32: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_FP32, 32);   \
+    case HSTU_PAGES_FP32 * 256 + 64: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_FP32, 64);   \
+    case HSTU_PAGES_FP32 * 256 + 96: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_FP32, 96);   \
+    case HSTU_PAGES_FP32 * 256 + 128: HSTU_PAGES_ROWS(KERNEL, HSTU_PAGES_FP32, 128); \
+    default: return cudaErrorInvalidValue;                                          \
   }
-  return cudaGetLastError();
+
+cudaError_t launch_pages_write(const PagesArgs& a, cudaStream_t st) {
+  HSTU_PAGES_DISPATCH(pages_write_kernel)
 }
 
 cudaError_t launch_pages_read(const PagesArgs& a, cudaStream_t st) {
-  if (a.R <= 0 || a.B <= 0) return cudaSuccess;
-  const unsigned blocks = unsigned((a.R + kRowWarps - 1) / kRowWarps);
-  switch (a.format) {
-    case HSTU_PAGES_BF16: pages_read_kernel<HSTU_PAGES_BF16><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    case HSTU_PAGES_FP32: pages_read_kernel<HSTU_PAGES_FP32><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    case HSTU_PAGES_E4M3: pages_read_kernel<HSTU_PAGES_E4M3><<<blocks, kRowWarps * 32, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  HSTU_PAGES_DISPATCH(pages_read_kernel)
 }
 
 }  // namespace hstu
