@@ -168,7 +168,7 @@ template <int FMT, int HD>
 struct Chunks {
   static constexpr int kElems = FMT == HSTU_PAGES_FP32 ? 4 : 8;   // elements of a chunk
   static constexpr int kPerHead = HD / kElems;
-  static constexpr int kBatch = 8;                                // of a lane, loaded at once
+  static constexpr int kBatch = 4;                                // of a lane, loaded at once
   int lane, H, shift;
   __device__ __forceinline__ Chunks(const PagesArgs& a)
       : lane(threadIdx.x & 31), H(a.H), shift(a.page_shift) {}
