@@ -201,7 +201,6 @@ struct PagesArgs {
   float* av;                 // [R, d] fp32
   float* partial;            // [num_sms * kPagesBlocksPerSm, 2, kPagesPartial]: parts of cut segments
   int32_t* tickets;          // [num_sms * kPagesBlocksPerSm]: parts that arrived; zero between calls
-  int min_units;             // fewest units a block takes
   int64_t wait_limit;        // bound of the pipeline waits in SM cycles (0: the default)
   int32_t* error;
   int num_sms;

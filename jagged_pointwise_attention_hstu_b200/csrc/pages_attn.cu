@@ -102,7 +102,8 @@ struct Shape {
   static constexpr int kPieces = kF32 ? 1 : (kF16 ? 2 : 3);
   static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 2 * NT);   // rows of q of a segment
   static constexpr int kTiles = (kGroup + 3) / 4;               // of 4 rows of q, for the scores
-  static constexpr int kRows = kF32 ? NT : 8 * NT;              // columns of P, rows of the sums
+  static constexpr int kColumns = 8 * NT;                       // of P
+  static constexpr int kRows = kF32 ? 4 : kGroup * kPieces;     // of the sums
   static constexpr int kRow = HD * (kF32 ? 4 : (kF16 ? 1 : 2)); // bytes of a key
   static constexpr int kBlocks = !kF32 && kRow == 64 ? 2 : 1;            // of 16 keys, a warp's step
   static constexpr int kStep = 16 * kBlocks;                    // keys of a warp's step
@@ -115,7 +116,7 @@ struct Shape {
   static constexpr int kDataBytes = 2 * kUnit * kRow;
   static constexpr int kSideBytes = 8 * kUnit + (kF16 ? 2 * kUnit : 0);
   static constexpr int kRingBytes(int stages) { return stages * (kDataBytes + kSideBytes); }
-  static constexpr int kStages = kRow == 256 ? 2 : 3;
+  static constexpr int kStages = kRow == 256 || kUnit * kRow > 8192 ? 2 : 3;
   static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT == 2 ? 2 : 3);
 };
 
@@ -152,9 +153,21 @@ __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err)
 
 // The block's run of units [u0, u1), the user it begins in and that user's
 // first unit; by the whole block (two barriers).  False: nothing to do.
+//
+// Block c begins at unit c * share, share the units of a block.  A cut costs the join of its parts
+// (2 to 3 us: the parts' way to memory, a ticket, the parts' way back), as much
+// as a few units: a segment that is at most kJoin units longer than a block's
+// share is not cut, its block takes it whole.
+constexpr int kJoin = 4;
+
+// a / b for a >= 0, b > 0: 64-bit division takes a hundred instructions
+__device__ __forceinline__ int64_t div64(int64_t a, int32_t b) {
+  return a <= int64_t(UINT32_MAX) ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
 struct Plan {
   int64_t scan[8];
-  int64_t start, share;
+  int64_t start, share, u0, u1;
   int32_t user;
 };
 
@@ -181,27 +194,41 @@ __device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl, int64_t&
     if (w < warp) before += pl.scan[w];
     total += pl.scan[w];
   }
-  // equal runs, but at least min_units: a cut costs a join
-  int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < a.min_units) share = a.min_units;
-  u0 = int64_t(blockIdx.x) * share;
-  if (u0 >= total) return false;
-  u1 = u0 + share < total ? u0 + share : total;
-  if (u0 >= before && u0 < before + mine) {
-    int64_t at = before;
-    int32_t b = tid * per;
-    for (;; ++b) {
-      int e = 0;
-      const int64_t k = user_of<S>(a, b, e).units;
-      if (u0 < at + k) break;
-      at += k;
-    }
-    pl.start = at;
-    pl.user = b;
+  const int64_t share = div64(total + gridDim.x - 1, gridDim.x);
+  const int64_t c0 = int64_t(blockIdx.x) * share, c1 = min(c0 + share, total);
+  if (c0 >= total) return false;
+  if (tid == 0) {
     pl.share = share;
+    if (c1 == total) pl.u1 = total;
+  }
+  // the threads that have the users of the two ends
+#pragma unroll
+  for (int end = 0; end < 2; ++end) {
+    const int64_t u = end == 0 ? c0 : c1;
+    if (u < before || u >= before + mine) continue;
+    int64_t at = before;
+    for (int32_t b = tid * per;; ++b) {
+      int e = 0;
+      const User x = user_of<S>(a, b, e);
+      if (u < at + x.units) {
+        const int64_t rel = u - at;
+        const int64_t cut = x.nu <= share + kJoin ? u - (rel - div64(rel, x.nu) * x.nu) : u;
+        if (end == 0) {
+          pl.u0 = cut;
+          pl.start = at;
+          pl.user = b;
+        } else {
+          pl.u1 = cut;
+        }
+        break;
+      }
+      at += x.units;
+    }
   }
   __syncthreads();
-  return true;
+  u0 = pl.u0;
+  u1 = pl.u1;
+  return u0 < u1;
 }
 
 // A block's part of one segment: tiles (units) [tile0, tile1) of row group
@@ -245,7 +272,7 @@ struct Walk {
       user = user_of<S>(a, b, e);
     }
     const int64_t rel = u - start;
-    const int32_t seg = user.units <= INT32_MAX ? int32_t(rel) / user.nu : int32_t(rel / user.nu);
+    const int32_t seg = int32_t(div64(rel, user.nu));
     const int32_t first = seg / a.H * S::kGroup;
     p.tile0 = int32_t(rel - int64_t(seg) * user.nu);
     p.tile1 = int64_t(user.nu - p.tile0) < u1 - u ? user.nu : int32_t(p.tile0 + (u1 - u));
@@ -254,9 +281,13 @@ struct Walk {
     p.nq = user.rows - first < S::kGroup ? user.rows - first : S::kGroup;
     p.n = user.n;
     p.row0 = user.r0 + first;
-    const int64_t seg0 = u - p.tile0;     // the segment's first unit
-    p.c0 = p.tile0 == 0 && p.tile1 == user.nu ? int32_t(blockIdx.x) : int32_t(seg0 / share);
-    p.c1 = p.tile0 == 0 && p.tile1 == user.nu ? p.c0 : int32_t((seg0 + user.nu - 1) / share);
+    p.c0 = p.c1 = int32_t(blockIdx.x);
+    if (p.tile0 != 0 || p.tile1 != user.nu) {
+      const int64_t seg0 = u - p.tile0;   // the segment's first unit
+      p.c0 = share <= INT32_MAX ? int32_t(div64(seg0, int32_t(share))) : int32_t(seg0 / share);
+      p.c1 = share <= INT32_MAX ? int32_t(div64(seg0 + user.nu - 1, int32_t(share)))
+                                : int32_t((seg0 + user.nu - 1) / share);
+    }
     u += p.tile1 - p.tile0;
     return true;
   }
@@ -314,12 +345,13 @@ __device__ __forceinline__ void self_terms(const PagesArgs& a, const Part& p, fl
 // left for the last block of the segment, which joins the parts in block order.
 // sync() is a barrier of these threads; it returns false to give up.
 template <class S, int HD, class Sum, class Self, class Sync>
-__device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, const Sum& sum,
+__device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, Sum& sum,
                                        const Self& self, int32_t* last, Sync sync) {
+  constexpr int kAll = kWarps * 32;
   const int tid = threadIdx.x;
   const bool whole = p.c0 == p.c1;
   float* part = a.partial + (int64_t(blockIdx.x) * 2 + (p.tile0 == 0 ? 1 : 0)) * (S::kGroup * HD);
-  for (int i = tid; i < p.nq * HD; i += kWarps * 32) {
+  for (int i = tid; i < p.nq * HD; i += kAll) {
     const int q = i / HD, c = i % HD;
     float x = 0.f;
 #pragma unroll
@@ -340,12 +372,33 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, const 
     }
     if (!sync()) return false;
     if (*last) {
+      // A thread has four columns of every kSlots-th part (a segment over the whole GPU has
+      // hundreds of parts, and one after the other their latency was the call's); the slots
+      // are added in order, through the shared memory of the sums.
       __threadfence();
-      for (int i = tid; i < p.nq * HD; i += kWarps * 32) {
-        float x = 0.f;
-        for (int32_t c = p.c0; c <= p.c1; ++c)
-          x += __ldcg(a.partial + (int64_t(c) * 2 + (c == p.c0 ? 1 : 0)) * (S::kGroup * HD) + i);
-        a.av[(p.row0 + i / HD) * a.d + p.h * HD + i % HD] = x / float(a.n_norm);
+      constexpr int kQuads = HD / 4, kSlots = kAll / kQuads;   // per row of the group
+      float* all = &sum[0][0][0];
+      static_assert(sizeof(sum) >= size_t(kSlots) * HD * 4, "slots");
+      const int quad = tid % kQuads, slot = tid / kQuads;
+      for (int q = 0; q < p.nq; ++q) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (slot < kSlots) {
+#pragma unroll 4
+          for (int32_t c = p.c0 + slot; c <= p.c1; c += kSlots) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(
+                a.partial + (int64_t(c) * 2 + (c == p.c0 ? 1 : 0)) * (S::kGroup * HD) + q * HD) + quad);
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+          }
+          *reinterpret_cast<float4*>(all + slot * HD + 4 * quad) = x;
+        }
+        if (!sync()) return false;
+        for (int i = tid; i < HD; i += kAll) {
+          float y = 0.f;
+#pragma unroll
+          for (int k = 0; k < kSlots; ++k) y += all[k * HD + i];
+          a.av[(p.row0 + q) * a.d + p.h * HD + i] = y / float(a.n_norm);
+        }
+        if (!sync()) return false;
       }
     }
   }
@@ -360,7 +413,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   constexpr int E = HD / 32;
   __shared__ Plan plan;
   __shared__ int4 s_time[128];
-  __shared__ float s_sum[kWarps][NT][S::kPad];
+  __shared__ __align__(16) float s_sum[kWarps][S::kRows][S::kPad];
   __shared__ float s_self[NT][HD];
   __shared__ int32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -475,7 +528,7 @@ struct Unit {
   int4 what;             // tile, runs (below) whose page index is none, Flag, cached rows
   Part part;
 };
-enum Flag { kFirst = 1, kLast = 2, kStop = 4 };   // of its part; no more units
+enum Flag { kLast = 1, kStop = 2 };   // of its part; no more units
 
 // untiled bulk copy global -> shared; all of dst, src and bytes multiples of 16
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -538,10 +591,10 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   __shared__ Plan plan;
   __shared__ Ring<S> ring;
   __shared__ int4 s_time[128];
-  __shared__ float s_sum[kWarps][S::kRows][S::kPad];
+  __shared__ __align__(16) float s_sum[kWarps][S::kRows][S::kPad];
   __shared__ float s_self[S::kGroup][HD];
   // P of a warp's step, a row per column of the operand
-  __shared__ __align__(16) uint16_t s_p[kWarps][S::kRows][S::kStep + 8];
+  __shared__ __align__(16) uint16_t s_p[kWarps][S::kColumns][S::kStep + 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long limit = a.wait_limit > 0 ? a.wait_limit : kWaitLimit;
   int64_t u0, u1;
@@ -591,8 +644,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         if (bad != 0) err |= HSTU_DEVERR_PAGES;
         if (lane == 0) {
           ring.unit[s].part = p;
-          ring.unit[s].what = make_int4(tile, int(bad), (tile == p.tile0 ? kFirst : 0) |
-                                        (tile + 1 == p.tile1 ? kLast : 0), p.n);
+          ring.unit[s].what = make_int4(tile, int(bad), tile + 1 == p.tile1 ? kLast : 0, p.n);
           mbar_arrive(&ring.head[s]);
           mbar_arrive_expect_tx(&ring.full[s], bytes);
         }
@@ -680,10 +732,11 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   fill_time(a, s_time, tid);
   bool up = sync(), done = false;
 
-  for (uint32_t k = 0; up; ++k) {
-    const int st = k % S::kStages;
-    const uint32_t parity = (k / S::kStages) & 1;
-    if (!__all_sync(0xffffffffu, wait_for(&ring.head[st], parity, limit))) break;
+  bool fresh = true;                           // the next unit begins a part, or there is none
+  uint32_t parity = 0;
+  for (int st = 0; up;) {
+    if (fresh && __any_sync(0xffffffffu, !wait_for(&ring.head[st], parity, limit))) break;
+    if (!fresh && __any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
     const int4 what = ring.unit[st].what;
     if (what.z & kStop) {
       done = true;
@@ -691,7 +744,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     }
     const int32_t tile = what.x, n = what.w;
 
-    if (what.z & kFirst) {
+    if (fresh) {
       // ---- a new part: q, and nothing summed; its pages are on their way
       const Part& p = ring.unit[st].part;
       nq = p.nq;
@@ -744,7 +797,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         }
       }
       __syncwarp();
-      for (int i = lane; i < S::kRows * (S::kStep + 8) / 2; i += 32)
+      for (int i = lane; i < S::kColumns * (S::kStep + 8) / 2; i += 32)
         reinterpret_cast<uint32_t*>(&ps[0][0])[i] = 0u;   // columns without a piece
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -756,8 +809,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       for (int i = 0; i < NT; ++i) inv[i] = __int_as_float((127 + 126) << 23);
       folds = chain = 0;
       if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
+      if (__any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
     }
-    if (!__all_sync(0xffffffffu, wait_for(&ring.full[st], parity, limit))) break;
 
     const int32_t k0 = warp * S::kStep, j0 = tile * S::kUnit + k0;   // the warp's keys
     if (j0 < n) {
@@ -954,6 +1007,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       for (int i = 0; i < NT; ++i) {
         const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
         const int r = 8 * i + 2 * t;
+        if (r >= S::kRows) continue;               // columns without a row of q
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const int dim = (S::kF16 ? g * (HD / 8) + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3));
@@ -982,6 +1036,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);
     }
+    fresh = (what.z & kLast) != 0;
+    if (++st == S::kStages) st = 0, parity ^= 1;
   }
   if (!done) err |= HSTU_DEVERR_TIMEOUT;
   if (err != 0) atomicOr(a.error, err);
@@ -1001,7 +1057,7 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
   using S = Shape<FMT, HD, NT>;
   static_assert(S::kPerSm <= kPagesBlocksPerSm, "workspace");
   static_assert(S::kGroup * HD <= kPagesPartial && S::kGroup <= 8, "workspace");
-  static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kRows, "operand");
+  static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kColumns, "operand");
   static_assert(S::kHalves * 128 >= S::kRow || !S::kSwizzle, "boxes");
   static_assert(S::kF32 || S::kRingBytes(S::kStages) <= 128 * 1024, "ring");
   if constexpr (S::kF32) {
@@ -1028,10 +1084,8 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_pages_attention(const PagesArgs& args, cudaStream_t st) {
-  if (args.R <= 0 || args.B <= 0) return cudaSuccess;
-  PagesArgs a = args;
-  a.min_units = 2;
+cudaError_t launch_pages_attention(const PagesArgs& a, cudaStream_t st) {
+  if (a.R <= 0 || a.B <= 0) return cudaSuccess;
   // more rows than users: candidates, so the variants that take more rows of a user at once
   const bool wide = a.R > a.B;
 #define HSTU_PAGES_ATTN(F, D) return wide ? launch<F, D, 2>(a, st) : launch<F, D, 1>(a, st)
