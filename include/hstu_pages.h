@@ -40,7 +40,7 @@ typedef enum { HSTU_PAGES_BF16 = 0, HSTU_PAGES_FP32 = 1, HSTU_PAGES_E4M3 = 2 } h
 typedef struct {
   hstu_page_format format;
   int32_t page_size;     /* rows of a page: 16, 32, 64, 128 or 256 */
-  int32_t num_pages;     /* >= 1 */
+  int32_t num_pages;     /* >= 1; num_pages * num_heads * 2 * page_size < 2^31 */
   void* kv;              /* [num_pages, num_heads, 2, page_size, head_dim]: plane 0 K, plane 1 V */
   uint8_t* scales;       /* E4M3: [num_pages, num_heads, 2, page_size]; else ignored */
   int64_t* timestamps;   /* [num_pages, page_size]; the layers of a stack may share one */
@@ -96,7 +96,8 @@ hstu_status hstu_pages_read(hstu_handle* h, const hstu_page_pool* pool, const in
  *   lengths      device int32 [num_users]: cached rows of each user, >= 0
  *   rab_pos, rab_time   as in hstu_layer_weights
  *   av           device fp32 [R, d]
- * Needs a fixed n_norm (> 0), as the history cache does; else HSTU_ERR_UNSUPPORTED. */
+ * Needs a fixed n_norm (> 0), as the history cache does, and
+ * R * num_heads * (table_width * page_size / 64 + 1) < 2^31; else HSTU_ERR_UNSUPPORTED. */
 hstu_status hstu_pages_attention(hstu_handle* h, const hstu_page_pool* pool, const void* uvqk,
                                  int64_t total_rows, const int32_t* seq_offsets,
                                  int32_t num_users, const int64_t* timestamps,

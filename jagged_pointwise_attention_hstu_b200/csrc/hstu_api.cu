@@ -1466,6 +1466,12 @@ hstu_status check_page_rows(const hstu_handle* h, int64_t R, const int32_t* offs
   return HSTU_OK;
 }
 
+// The attention's pieces of work (64 keys at least, of one head and row) are counted in 32 bits.
+bool attention_fits(const hstu_handle* h, int64_t R, int32_t width, int32_t page_size) {
+  const int64_t keys = int64_t(width) * page_size / 64 + 1;
+  return R <= INT32_MAX / (keys * h->cfg.num_heads);
+}
+
 hstu_status check_ptrs(std::initializer_list<const void*> ps) {
   for (const void* p : ps)
     if (p == nullptr || !hstu::aligned16(p)) return HSTU_ERR_INVALID_ARG;
@@ -1564,6 +1570,7 @@ hstu_status hstu_pages_attention(hstu_handle* h, const hstu_page_pool* pool, con
   if (s != HSTU_OK) return s;
   if (h->cfg.n_norm <= 0) return HSTU_ERR_UNSUPPORTED;
   if (R == 0) return HSTU_OK;
+  if (!attention_fits(h, R, width, pool->page_size)) return HSTU_ERR_UNSUPPORTED;
   s = check_ptrs({uvqk, ts, rab_pos, rab_time, av});
   if (s != HSTU_OK || lengths == nullptr) return HSTU_ERR_INVALID_ARG;
   const DeviceGuard guard(h->device);
@@ -1627,6 +1634,7 @@ hstu_status hstu_pages_step(hstu_handle* h, const hstu_page_pool* pools, const v
     if (s == HSTU_OK) s = check_pool(h, &pools[l], true);
     if (s == HSTU_OK) s = check_page_rows(h, R, offsets, B, table, width, pools[l].page_size);
     if (s != HSTU_OK) return s;
+    if (R > 0 && !attention_fits(h, R, width, pools[l].page_size)) return HSTU_ERR_UNSUPPORTED;
   }
   if (h->cfg.n_norm <= 0) return HSTU_ERR_UNSUPPORTED;
   if (R == 0) return HSTU_OK;

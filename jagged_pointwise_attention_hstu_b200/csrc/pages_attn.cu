@@ -121,114 +121,147 @@ struct Shape {
 };
 
 struct User {
-  int64_t r0, units;
+  int64_t r0;
   int32_t rows, n, nu;   // rows of the call, cached rows, units of one segment
+  int32_t segments;      // groups of rows * heads; none for an ill-formed user (err says why)
 };
 
-// A user's share of the work; an ill-formed user has none (err says why).
+// A user's share of the work.  The units of a call are fewer than 2^31: the entry point sees
+// to that.
 template <class S>
 __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err) {
   User u;
-  const int64_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
-  const int64_t n = __ldg(a.lengths + b);
+  const int32_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
+  u.n = __ldg(a.lengths + b);
+  if (r0 < 0 || r1 < r0 || r1 > a.R || (b == 0 && r0 != 0)) err |= HSTU_DEVERR_OFFSETS;
+  if (u.n < 0 || u.n > (a.width << a.page_shift)) err |= HSTU_DEVERR_PAGES;
   u.r0 = r0;
-  u.units = 0;
-  u.rows = 0;
-  u.n = 0;
-  u.nu = 1;
-  if (r0 < 0 || r1 < r0 || r1 > a.R || (b == 0 && r0 != 0)) {
-    err |= HSTU_DEVERR_OFFSETS;
-    return u;
-  }
-  if (n < 0 || n > (a.width << a.page_shift)) {
-    err |= HSTU_DEVERR_PAGES;
-    return u;
-  }
-  u.rows = int32_t(r1 - r0);
-  u.n = int32_t(n);
-  u.nu = n == 0 ? 1 : int32_t((n + S::kUnit - 1) / S::kUnit);
-  u.units = int64_t((u.rows + S::kGroup - 1) / S::kGroup) * a.H * u.nu;
+  u.rows = err == 0 ? r1 - r0 : 0;
+  u.nu = err == 0 && u.n > 0 ? (u.n + S::kUnit - 1) / S::kUnit : 1;
+  u.segments = (u.rows + S::kGroup - 1) / S::kGroup * a.H;
   return u;
 }
 
-// The block's run of units [u0, u1), the user it begins in and that user's
-// first unit; by the whole block (two barriers).  False: nothing to do.
+// The block's work.  share: the units of a block if all had as many.
 //
-// Block c begins at unit c * share, share the units of a block.  A cut costs the join of its parts
-// (2 to 3 us: the parts' way to memory, a ticket, the parts' way back), as much
-// as a few units: a segment that is at most kJoin units longer than a block's
-// share is not cut, its block takes it whole.
+// Parts, if every block can have one part of one segment, of at most `share`
+// units: then it does, the segments cut into equal parts.  Else runs: block c has
+// the units from c * share on, whatever segments they belong to; but a segment at
+// most kJoin units longer than that is not cut, the block it begins in takes it
+// whole.  A cut costs the join of its parts (2 to 3 us: the parts' way to memory, a
+// ticket, the parts' way back), as much as a few units, and a block with the
+// ends of two segments pays for two.  (16 users of up to 4096 rows, d 512: runs
+// 15.9 us, parts 13.8; 1 of 100003: 32.9 and 30.7.)
 constexpr int kJoin = 4;
-
-// a / b for a >= 0, b > 0: 64-bit division takes a hundred instructions
-__device__ __forceinline__ int64_t div64(int64_t a, int32_t b) {
-  return a <= int64_t(UINT32_MAX) ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
-}
+constexpr int32_t kWarpUsers = 256;   // with more users all threads plan, not one warp
 
 struct Plan {
-  int64_t scan[8];
-  int64_t start, share, u0, u1;
-  int32_t user;
+  int32_t sums[8];
+  int32_t start, share, u0, u1;   // runs: the first user's first unit, the run
+  int32_t user;                   // of the part, or the first of the run
+  int32_t item, pieces;           // parts: the user's part, parts of a segment (0: runs)
 };
 
-template <class S>
-__device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl, int64_t& u0, int64_t& u1) {
-  constexpr int kAll = S::kThreads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t per = (a.B + kAll - 1) / kAll;
+// The threads that make the plan: one warp, or all kAll of the block.
+template <int kAll>
+struct Team {
+  static __device__ __forceinline__ int rank() { return kAll == 32 ? threadIdx.x & 31 : threadIdx.x; }
+  static __device__ __forceinline__ void sync() {
+    if (kAll == 32) __syncwarp();
+    else __syncthreads();
+  }
+  // Sum of each thread's x, and that of the threads before; `sums` may be used again behind a sync.
+  static __device__ __forceinline__ int32_t scan(int32_t x, int32_t* sums, int32_t& before) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    before = inc - x;
+    if (kAll == 32) return __shfl_sync(0xffffffffu, inc, 31);
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kAll / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    return total;
+  }
+};
+
+// By the whole team; `pl` is the team's own.  False: nothing to do.  Small code
+// (loops that are not unrolled, 32 bits): every instruction of it is new to the SM.
+template <class S, int kAll>
+__device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl) {
+  using T = Team<kAll>;
+  const int tid = T::rank();
+  const int32_t per = (a.B + kAll - 1) / kAll, b0 = tid * per, b1 = min(b0 + per, a.B);
   int err = 0;
-  int64_t mine = 0;
-  for (int32_t b = tid * per; b < (tid + 1) * per && b < a.B; ++b) mine += user_of<S>(a, b, err).units;
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
+  int32_t mine = 0, before;
+#pragma unroll 1
+  for (int32_t b = b0; b < b1; ++b) {
+    int e = 0;
+    const User x = user_of<S>(a, b, e);
+    mine += x.segments * x.nu;
+    err |= e;
   }
-  if (lane == 31) pl.scan[warp] = inc;
-  if (blockIdx.x == 0 && err != 0) atomicOr(a.error, err);
-  __syncthreads();
-  int64_t before = inc - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAll / 32; ++w) {
-    if (w < warp) before += pl.scan[w];
-    total += pl.scan[w];
+  const int32_t total = T::scan(mine, pl.sums, before);
+  if (blockIdx.x == 0 && err != 0) atomicOr(a.error, err);   // by every team alike
+  if (total == 0) return false;
+  const int32_t share = (total + gridDim.x - 1) / gridDim.x;
+  T::sync();
+  int32_t items = 0, items_before;
+#pragma unroll 1
+  for (int32_t b = b0; b < b1; ++b) {
+    int e = 0;
+    const User x = user_of<S>(a, b, e);
+    items += x.segments * ((x.nu + share - 1) / share);
   }
-  const int64_t share = div64(total + gridDim.x - 1, gridDim.x);
-  const int64_t c0 = int64_t(blockIdx.x) * share, c1 = min(c0 + share, total);
-  if (c0 >= total) return false;
+  const int32_t parts = T::scan(items, pl.sums, items_before);
+  const bool runs = parts > int32_t(gridDim.x);
+  const int32_t c = blockIdx.x;
+  const int32_t c0 = c * share, c1 = total - c0 > share ? c0 + share : total;
+  if (runs ? c0 >= total : c >= parts) return false;
   if (tid == 0) {
     pl.share = share;
+    if (runs) pl.pieces = 0;
     if (c1 == total) pl.u1 = total;
   }
-  // the threads that have the users of the two ends
-#pragma unroll
-  for (int end = 0; end < 2; ++end) {
-    const int64_t u = end == 0 ? c0 : c1;
-    if (u < before || u >= before + mine) continue;
-    int64_t at = before;
-    for (int32_t b = tid * per;; ++b) {
+  // the threads that have the block's part, or the users of the two ends of its run
+#pragma unroll 1
+  for (int end = 0; end < (runs ? 2 : 1); ++end) {
+    const int32_t u = runs ? (end == 0 ? c0 : c1) : c;
+    int32_t at = runs ? before : items_before;
+    if (u < at || u >= at + (runs ? mine : items)) continue;
+#pragma unroll 1
+    for (int32_t b = b0;; ++b) {
       int e = 0;
       const User x = user_of<S>(a, b, e);
-      if (u < at + x.units) {
-        const int64_t rel = u - at;
-        const int64_t cut = x.nu <= share + kJoin ? u - (rel - div64(rel, x.nu) * x.nu) : u;
-        if (end == 0) {
-          pl.u0 = cut;
-          pl.start = at;
-          pl.user = b;
-        } else {
+      const int32_t pieces = runs ? x.nu : (x.nu + share - 1) / share;
+      const int32_t k = x.segments * pieces;
+      if (u < at + k) {
+        const int32_t rel = u - at;
+        const int32_t cut = x.nu <= share + kJoin ? u - rel % x.nu : u;
+        if (end == 1) {
           pl.u1 = cut;
+        } else {
+          pl.user = b;
+          pl.start = at;
+          pl.u0 = cut;
+          pl.item = rel;
+          if (!runs) pl.pieces = pieces;
         }
         break;
       }
-      at += x.units;
+      at += k;
     }
   }
-  __syncthreads();
-  u0 = pl.u0;
-  u1 = pl.u1;
-  return u0 < u1;
+  T::sync();
+  return !runs || pl.u0 < pl.u1;
 }
 
 // A block's part of one segment: tiles (units) [tile0, tile1) of row group
@@ -241,54 +274,65 @@ struct Part {
   int32_t c0, c1;        // the first and last block that have a part
 };
 
-// Walks the block's run part by part (one warp, or all alike).
+// Walks the block's work part by part (one warp, or all alike).
 template <class S>
 struct Walk {
-  int64_t u, u1, start, share;
-  int32_t b;
+  int32_t u, u1, start, share, b, item, pieces;
   User user;
-  __device__ __forceinline__ Walk(const PagesArgs& a, const Plan& pl, int64_t u0, int64_t end)
-      : u(u0), u1(end), start(pl.start), share(pl.share), b(pl.user) {
+  __device__ __forceinline__ Walk(const PagesArgs& a, const Plan& pl, bool any)
+      : u(pl.u0), u1(pl.u1), start(pl.start), share(pl.share), b(pl.user), item(pl.item),
+        pieces(pl.pieces) {
     int e = 0;
-    user = user_of<S>(a, b, e);
+    if (any) user = user_of<S>(a, b, e);
   }
   __device__ __forceinline__ bool next(const PagesArgs& a, Part& p) {
-    if (u >= u1) return false;
-    if (u >= start + user.units) {        // the next user that has rows
-      start += user.units;
-      for (;;) {
-        const int32_t c = b + 1 + int32_t(threadIdx.x & 31);
-        int e = 0;
-        const bool has = c < a.B && user_of<S>(a, c, e).units > 0;
-        const unsigned m = __ballot_sync(0xffffffffu, has);
-        if (m != 0) {
-          b += __ffs(m);
-          break;
+    int32_t seg;
+    p.c0 = p.c1 = int32_t(blockIdx.x);
+    if (pieces != 0) {                    // one part of one segment
+      if (item < 0) return false;
+      seg = item / pieces;
+      const int32_t k = item - seg * pieces;
+      p.tile0 = int32_t(int64_t(k) * user.nu / pieces);
+      p.tile1 = int32_t(int64_t(k + 1) * user.nu / pieces);
+      p.c0 -= k;
+      p.c1 = p.c0 + pieces - 1;
+      item = -1;
+    } else {
+      if (u >= u1) return false;
+      if (u >= start + user.segments * user.nu) {   // the next user that has rows
+        start += user.segments * user.nu;
+        for (;;) {
+          const int32_t c = b + 1 + int32_t(threadIdx.x & 31);
+          int e = 0;
+          const bool has = c < a.B && user_of<S>(a, c, e).segments > 0;
+          const unsigned m = __ballot_sync(0xffffffffu, has);
+          if (m != 0) {
+            b += __ffs(m);
+            break;
+          }
+          b += 32;
+          if (b >= a.B) return false;     // cannot happen: u < total
         }
-        b += 32;
-        if (b >= a.B) return false;       // cannot happen: u < total
+        int e = 0;
+        user = user_of<S>(a, b, e);
       }
-      int e = 0;
-      user = user_of<S>(a, b, e);
+      const int32_t rel = u - start;
+      seg = rel / user.nu;
+      p.tile0 = rel - seg * user.nu;
+      p.tile1 = min(user.nu, p.tile0 + (u1 - u));
+      if (p.tile0 != 0 || p.tile1 != user.nu) {
+        const int32_t seg0 = u - p.tile0;   // the segment's first unit
+        p.c0 = seg0 / share;
+        p.c1 = (seg0 + user.nu - 1) / share;
+      }
+      u += p.tile1 - p.tile0;
     }
-    const int64_t rel = u - start;
-    const int32_t seg = int32_t(div64(rel, user.nu));
     const int32_t first = seg / a.H * S::kGroup;
-    p.tile0 = int32_t(rel - int64_t(seg) * user.nu);
-    p.tile1 = int64_t(user.nu - p.tile0) < u1 - u ? user.nu : int32_t(p.tile0 + (u1 - u));
     p.b = b;
     p.h = seg % a.H;
-    p.nq = user.rows - first < S::kGroup ? user.rows - first : S::kGroup;
+    p.nq = min(user.rows - first, S::kGroup);
     p.n = user.n;
     p.row0 = user.r0 + first;
-    p.c0 = p.c1 = int32_t(blockIdx.x);
-    if (p.tile0 != 0 || p.tile1 != user.nu) {
-      const int64_t seg0 = u - p.tile0;   // the segment's first unit
-      p.c0 = share <= INT32_MAX ? int32_t(div64(seg0, int32_t(share))) : int32_t(seg0 / share);
-      p.c1 = share <= INT32_MAX ? int32_t(div64(seg0 + user.nu - 1, int32_t(share)))
-                                : int32_t((seg0 + user.nu - 1) / share);
-    }
-    u += p.tile1 - p.tile0;
     return true;
   }
 };
@@ -363,10 +407,11 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, Sum& s
     else part[i] = x;
   }
   if (!whole) {
-    __threadfence();
     if (!sync()) return false;
     if (tid == 0) {
-      const int32_t k = atomicAdd(a.tickets + p.c0, 1);
+      int32_t k;                                   // behind the barrier: releases all threads' parts
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                   : "=r"(k) : "l"(a.tickets + p.c0) : "memory");
       *last = k == p.c1 - p.c0 ? 1 : 0;
       if (*last) a.tickets[p.c0] = 0;              // as the next call expects it
     }
@@ -375,7 +420,6 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, Sum& s
       // A thread has four columns of every kSlots-th part (a segment over the whole GPU has
       // hundreds of parts, and one after the other their latency was the call's); the slots
       // are added in order, through the shared memory of the sums.
-      __threadfence();
       constexpr int kQuads = HD / 4, kSlots = kAll / kQuads;   // per row of the group
       float* all = &sum[0][0][0];
       static_assert(sizeof(sum) >= size_t(kSlots) * HD * 4, "slots");
@@ -411,17 +455,19 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
     pages_attention_f32_kernel(const PagesArgs a) {
   using S = Shape<HSTU_PAGES_FP32, HD, NT>;
   constexpr int E = HD / 32;
-  __shared__ Plan plan;
+  __shared__ Plan plans[kWarps];
   __shared__ int4 s_time[128];
   __shared__ __align__(16) float s_sum[kWarps][S::kRows][S::kPad];
   __shared__ float s_self[NT][HD];
   __shared__ int32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k4 = lane >> 3, t8 = lane & 7;
-  int64_t u0, u1;
   fill_time(a, s_time, tid);
-  if (!make_plan<S>(a, plan, u0, u1)) return;
-  Walk<S> walk(a, plan, u0, u1);
+  const bool alone = a.B <= kWarpUsers;      // a warp plans for itself
+  Plan& plan = plans[alone ? warp : 0];
+  if (!(alone ? make_plan<S, 32>(a, plan) : make_plan<S, S::kThreads>(a, plan))) return;
+  __syncthreads();
+  Walk<S> walk(a, plan, true);
   const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
   const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
   const int32_t slot_mask = (1 << a.page_shift) - 1;
@@ -597,7 +643,6 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   __shared__ __align__(16) uint16_t s_p[kWarps][S::kColumns][S::kStep + 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long limit = a.wait_limit > 0 ? a.wait_limit : kWaitLimit;
-  int64_t u0, u1;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&ring.head[s], 1);
@@ -607,18 +652,22 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     mbar_init(&ring.turn, kWarps);
     fence_mbarrier_init();
   }
-  if (!make_plan<S>(a, plan, u0, u1)) return;
+  __syncthreads();
+  // what there is to do is the producer's to know; with many users all threads plan
+  const bool alone = a.B <= kWarpUsers;
+  if (!alone && !make_plan<S, S::kThreads>(a, plan)) return;
   const int32_t run_shift = (1 << a.page_shift) < S::kUnit ? a.page_shift : 31 - __clz(S::kUnit);
   const int32_t run = 1 << run_shift;
   int err = 0;
 
   if (warp == kWarps) {
     // ---- the producer
-    Walk<S> walk(a, plan, u0, u1);
+    const bool any = !alone || make_plan<S, 32>(a, plan);
+    Walk<S> walk(a, plan, any);
     Part p;
     uint32_t issued = 0;                 // units put into the ring
     bool ok = true;
-    while (ok && walk.next(a, p)) {
+    while (ok && any && walk.next(a, p)) {
       const int32_t* table = a.table + int64_t(p.b) * a.width;
       auto page_of = [&](int32_t tile) { // of the lane's run; -1: no key there, -2: no such page
         const int64_t j = int64_t(tile) * S::kUnit + (int64_t(lane) << run_shift);
@@ -1046,8 +1095,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
 // No more blocks than there can be units.
 template <class S>
 unsigned grid_of(const PagesArgs& a) {
-  const int64_t keys = (a.width << a.page_shift) / S::kUnit + 1;
-  const int64_t most = a.R < INT32_MAX / (a.H * keys) ? a.R * a.H * keys : INT32_MAX;
+  const int64_t most = a.R * a.H * ((a.width << a.page_shift) / S::kUnit + 1);
   const int64_t grid = int64_t(a.num_sms) * S::kPerSm;
   return unsigned(grid < most ? grid : most);
 }
