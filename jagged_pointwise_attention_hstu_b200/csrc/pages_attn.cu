@@ -153,7 +153,7 @@ __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err)
 // ends of two segments pays for two.  (16 users of up to 4096 rows, d 512: runs
 // 15.9 us, parts 13.8; 1 of 100003: 32.9 and 30.7.)
 constexpr int kJoin = 4;
-constexpr int32_t kWarpUsers = 256;   // with more users all threads plan, not one warp
+constexpr int32_t kWarpUsers = 64;   // with more users all threads plan, not one warp
 
 struct Plan {
   int32_t sums[8];
