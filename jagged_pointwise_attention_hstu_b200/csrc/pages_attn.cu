@@ -351,11 +351,11 @@ __device__ __forceinline__ float bias_of(const PagesArgs& a, const int4* s_time,
                                          int32_t n, int32_t j, int64_t now, int64_t then) {
   const float pos = n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
   const int64_t gap = int64_t(uint64_t(now) - uint64_t(then));
-  if (a.lut_exact && gap < 0x7FFFFFFE) {
-    const uint32_t x = gap > 0 ? uint32_t(gap) + 1u : 1u;
-    const int z = __clz(x);
-    const int4 bin = s_time[(31 - z) * 4 + ((x << z) >> 29 & 3)];
-    return pos + __int_as_float(gap >= bin.x ? bin.z : bin.y);
+  const uint32_t lo = uint32_t(gap);
+  if (a.lut_exact && uint32_t(uint64_t(gap) >> 32) == 0 && lo < 0x7FFFFFFEu) {
+    // bin 4e + m of gap + 1: the exponent and the first two bits of its mantissa
+    const int4 bin = s_time[(__float_as_uint(__uint2float_rz(lo + 1u)) >> 21) - 4 * 127];
+    return pos + __int_as_float(lo >= uint32_t(bin.x) ? bin.z : bin.y);
   }
   return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
 }
@@ -774,8 +774,27 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   auto key_of = [&](int i) { return S::kSwizzle ? 2 * t + (i & 1) + 8 * (i >> 1) : t + 4 * i; };
   const int spot = (lane & 16) + (S::kSwizzle ? 4 * (lane >> 1 & 3) + (lane & 1) + 2 * (lane >> 3 & 1)
                                               : 4 * (lane & 3) + (lane >> 2 & 3));
+  // byte offsets that do not change: of the warp's blocks in a stage, of the lane's chunks of a
+  // block's keys, and of its rows and chunks of the values (b: the low bit of chunk or row)
+  uint32_t block_at[NB], k_at[2], v_at[2];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int32_t kb = warp * S::kStep + 16 * nb;
+    block_at[nb] = ((kb >> run_shift) << (run_shift + 1)) * S::kRow +
+                   (kb & (run - 1)) * (S::kSwizzle ? 128 : S::kRow);
+  }
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    k_at[b] = S::kSwizzle ? g * 128 + (((2 * t + b) ^ g) << 4) : g * S::kRow + 16 * t;
+    v_at[b] = S::kSwizzle ? (2 * t + b) * 128 + ((g ^ (2 * t + b)) << 4) : t * S::kRow + 8 * g;
+  }
+  const uint32_t half_at = run * 128, plane_at = run * S::kRow;
+  const int32_t kl = warp * S::kStep + (lane & (S::kStep - 1));   // the lane's own key of a unit
+  // its scales: [run][plane][key]
+  const int32_t scale_at = 8 * S::kUnit + ((kl >> run_shift) << (run_shift + 1)) + (kl & (run - 1));
   uint32_t qb[QT][KS][2];
-  float q_scale[QT], inv[NT], acc[MT][NT][4];
+  // e4m3: the rows' scales of q, and what keeps their P within fp16
+  float q_scale[S::kGroup], inv[S::kGroup], acc[MT][NT][4];
   int64_t row0 = 0, now0 = 0;
   int nq = 1, folds = 0, chain = 0;
   fill_time(a, s_time, tid);
@@ -807,7 +826,6 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         const bool odd = (g & 1) != 0;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(a.uvqk) + (row0 + q) * 4 * a.d + 2 * a.d + p.h * HD);
-        q_scale[i] = 1.f;
         if constexpr (!S::kF16) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
@@ -831,8 +849,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           int e = int(__float_as_uint(m) >> 23) - 127 - 14;
           e = e < -126 ? -126 : (e > 112 ? 112 : e);
-          q_scale[i] = __int_as_float((e + 127) << 23);
-          const float f = __int_as_float((127 - e) << 23);
+          const float qs = __int_as_float((e + 127) << 23), f = __int_as_float((127 - e) << 23);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) q_scale[4 * i + c] = __shfl_sync(0xffffffffu, qs, 8 * c);
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -852,10 +871,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
-      // fp16 pieces: P times a power of two of its row stays below 2^15; inv is that of the row
-      // whose two pieces are the lane's columns (row t of the tile)
+      // fp16 pieces: P times a power of two of its row, inv, stays below 2^15
 #pragma unroll
-      for (int i = 0; i < NT; ++i) inv[i] = __int_as_float((127 + 126) << 23);
+      for (int i = 0; i < S::kGroup; ++i) inv[i] = __int_as_float((127 + 126) << 23);
       folds = chain = 0;
       if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
       if (__any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
@@ -864,25 +882,19 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     const int32_t k0 = warp * S::kStep, j0 = tile * S::kUnit + k0;   // the warp's keys
     if (j0 < n) {
       const uint32_t data = smem_u32(stages) + st * S::kDataBytes;
-      // the lane's own key; scales are [run][plane][key]
-      const int32_t kl = k0 + (lane & (S::kStep - 1)), jl = tile * S::kUnit + kl;
-      const bool mine = jl < n && !(uint32_t(what.y) >> (kl >> run_shift) & 1);
+      const int32_t jl = tile * S::kUnit + kl;
+      bool mine = jl < n;
+      if (what.y != 0) mine = mine && !(uint32_t(what.y) >> (kl >> run_shift) & 1);
       const uint8_t* side = stages + S::kStages * S::kDataBytes + st * S::kSideBytes;
       const int64_t then = *reinterpret_cast<const int64_t*>(side + 8 * kl);
       float ks = 1.f, vs = 1.f;
       if constexpr (S::kF16) {
-        const uint8_t* sc = side + 8 * S::kUnit + ((kl >> run_shift) << (run_shift + 1)) + (kl & (run - 1));
-        ks = block_scale(sc[0]);
-        vs = block_scale(sc[run]);
+        ks = block_scale(side[scale_at]);
+        vs = block_scale(side[scale_at + run]);
       }
       float s[NB][2][QT];                // of key 16 nb + 8 x + g and row 4i + t
-      uint32_t at[NB];                   // the blocks' runs of keys
-      int32_t key0[NB];                  // and their first keys there
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const int32_t kb = k0 + 16 * nb;
-        at[nb] = data + ((kb >> run_shift) << (run_shift + 1)) * S::kRow;
-        key0[nb] = kb & (run - 1);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float c[QT][4];
@@ -890,10 +902,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           for (int i = 0; i < QT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
 #pragma unroll
           for (int y = 0; y < KC; ++y) {
-            const uint32_t r = key0[nb] + 8 * x + g, c16 = chunk(y);
-            const uint4 v = lds16(S::kSwizzle ? at[nb] + ((c16 >> 3) * run + r) * 128 +
-                                                    (((c16 & 7) ^ g) << 4)
-                                              : at[nb] + r * S::kRow + 16 * c16);
+            const uint4 v = lds16(data + block_at[nb] + k_at[y & 1] + (y >> 1) * half_at +
+                                  8 * x * (S::kSwizzle ? 128 : S::kRow));
             if constexpr (S::kF16) {
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -932,7 +942,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
             const float z = lane & 8 ? y3 : y2;
             y[c] = lane & 16 ? z : y[c];
           }
-          if constexpr (S::kF16) y[c] = y[c] * __shfl_sync(0xffffffffu, q_scale[i], 8 * c) * ks;
+          if constexpr (S::kF16) y[c] = y[c] * q_scale[4 * i + c] * ks;
           int64_t now = now0;
           if (4 * i + c > 0) now = __ldg(a.ts + row0 + (4 * i + c < nq ? 4 * i + c : nq - 1));
           y[c] = silu(y[c] + bias_of(a, s_time, pos_far, n, jl, now, then));
@@ -940,26 +950,21 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           y[c] = mine ? y[c] : 0.f;      // no key here: what memory holds must not reach the sum
         }
         if constexpr (S::kF16) {         // four rows a tile of scores, and a tile of P
-          float f[N];
           bool over = false;
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
-            f[c] = __shfl_sync(0xffffffffu, inv[i], c);
-            over |= fabsf(y[c]) * f[c] > 32768.f;
-          }
+          for (int c = 0; c < N; ++c) over |= fabsf(y[c]) * inv[4 * i + c] > 32768.f;
           if (__any_sync(0xffffffffu, over)) {                       // raise a row's power
 #pragma unroll
             for (int c = 0; c < N; ++c) {
               float m = fabsf(y[c]);
 #pragma unroll
               for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-              if (!(m * f[c] > 32768.f)) continue;
+              if (!(m * inv[4 * i + c] > 32768.f)) continue;
               int e = int(__float_as_uint(m) >> 23) - 127 - 6;       // to [2^6, 2^7): room to grow
               e = e > 126 ? 126 : (e < -126 ? -126 : e);
-              const float f1 = __int_as_float((127 - e) << 23);
-              const float ratio = t == c ? f1 / f[c] : 1.f;
-              if (t == c) inv[i] = f1;
-              f[c] = f1;
+              const float f = __int_as_float((127 - e) << 23);
+              const float ratio = t == c ? f / inv[4 * i + c] : 1.f;   // columns 2t, 2t + 1: row t
+              inv[4 * i + c] = f;
 #pragma unroll
               for (int m2 = 0; m2 < MT; ++m2) {
                 acc[m2][i][0] *= ratio, acc[m2][i][1] *= ratio;
@@ -969,7 +974,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           }
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            y[c] *= f[c];
+            y[c] *= inv[4 * i + c];
             const __half hi = __float2half_rn(y[c]);
             const __half lo = __float2half_rn(y[c] - __half2float(hi));
             if (S::kStep == 32 || lane < S::kStep) {
@@ -1009,16 +1014,15 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         uint32_t v[4][VW];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t r = key0[nb] + key_of(i);
-          const uint32_t row = at[nb] + run * S::kRow +
-                               (S::kSwizzle ? r * 128 + ((g ^ (r & 7)) << 4) : r * S::kRow + 8 * g);
+          const uint32_t row = data + block_at[nb] + plane_at + v_at[i & (S::kSwizzle ? 1 : 0)] +
+                               (S::kSwizzle ? (i >> 1) * 1024 : i * 4 * S::kRow);
           if constexpr (VW == 2) {
             const uint2 x = lds8(row);
             v[i][0] = x.x, v[i][1] = x.y;
           } else {
 #pragma unroll
             for (int c = 0; c < VW / 4; ++c) {
-              const uint4 x = lds16(row + 128 * run * c);
+              const uint4 x = lds16(row + half_at * c);
               v[i][4 * c] = x.x, v[i][4 * c + 1] = x.y, v[i][4 * c + 2] = x.z, v[i][4 * c + 3] = x.w;
             }
           }
@@ -1054,7 +1058,11 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     if (chain == kFold || (what.z & kLast)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const float scale = S::kF16 ? 1.f / inv[i] : 1.f;
+        float scale = 1.f;                         // of row t of the tile
+        if constexpr (S::kF16) {
+          const float f01 = t & 1 ? inv[4 * i + 1] : inv[4 * i], f23 = t & 1 ? inv[4 * i + 3] : inv[4 * i + 2];
+          scale = 1.f / (t & 2 ? f23 : f01);
+        }
         const int r = 8 * i + 2 * t;
         if (r >= S::kRows) continue;               // columns without a row of q
 #pragma unroll
