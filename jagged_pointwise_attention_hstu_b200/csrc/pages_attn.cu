@@ -346,18 +346,26 @@ __device__ __forceinline__ void fill_time(const PagesArgs& a, int4* s_time, int 
                         __float_as_int(__ldg(a.rab_time + next)), 0);
 }
 
-// The two biases of a row at time `now` for key j at time `then`.
-__device__ __forceinline__ float bias_of(const PagesArgs& a, const int4* s_time, float pos_far,
-                                         int32_t n, int32_t j, int64_t now, int64_t then) {
-  const float pos = n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
-  const int64_t gap = int64_t(uint64_t(now) - uint64_t(then));
-  const uint32_t lo = uint32_t(gap);
-  if (a.lut_exact && uint32_t(uint64_t(gap) >> 32) == 0 && lo < 0x7FFFFFFEu) {
-    // bin 4e + m of gap + 1: the exponent and the first two bits of its mantissa
-    const int4 bin = s_time[(__float_as_uint(__uint2float_rz(lo + 1u)) >> 21) - 4 * 127];
-    return pos + __int_as_float(lo >= uint32_t(bin.x) ? bin.z : bin.y);
-  }
-  return pos + __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
+// rab_pos for key j of the n cached, with pos_far what most have.
+__device__ __forceinline__ float pos_bias(const PagesArgs& a, float pos_far, int32_t n, int32_t j) {
+  return n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
+}
+
+// Whether the bins serve a gap (from 0 to 2^31 - 3 s), and what they say: bin 4e + m of
+// gap + 1 has the exponent and the first two bits of the mantissa.
+__device__ __forceinline__ bool bin_gap(const PagesArgs& a, int64_t gap) {
+  return a.lut_exact && uint32_t(uint64_t(gap) >> 32) == 0 && uint32_t(gap) < 0x7FFFFFFEu;
+}
+__device__ __forceinline__ float bin_bias(const int4* s_time, uint32_t gap) {
+  const int4 bin = s_time[(__float_as_uint(__uint2float_rz(gap + 1u)) >> 21) - 4 * 127];
+  return __int_as_float(gap >= uint32_t(bin.x) ? bin.z : bin.y);
+}
+__device__ __forceinline__ float time_bias(const PagesArgs& a, const int4* s_time, int64_t gap) {
+  return bin_gap(a, gap) ? bin_bias(s_time, uint32_t(gap))
+                         : __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
+}
+__device__ __forceinline__ int64_t gap_of(int64_t now, int64_t then) {
+  return int64_t(uint64_t(now) - uint64_t(then));   // any two timestamps: no signed overflow
 }
 
 // What each row adds of itself, SiLU(s_r) v_r: a warp a row.
@@ -504,7 +512,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
           const int64_t then = __ldg(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
           float bias[NT];                // of the lane's key
 #pragma unroll
-          for (int i = 0; i < NT; ++i) bias[i] = bias_of(a, s_time, pos_far, n, jl, now[i], then);
+          for (int i = 0; i < NT; ++i)
+            bias[i] = pos_bias(a, pos_far, n, jl) + time_bias(a, s_time, gap_of(now[i], then));
           const float* base = static_cast<const float*>(a.kv) +
               ((((int64_t(page) * a.H + p.h) * 2) << a.page_shift) + (j0 & slot_mask)) * HD;
           float4 k[4][E], v[4][E];
@@ -639,6 +648,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   __shared__ int4 s_time[128];
   __shared__ __align__(16) float s_sum[kWarps][S::kRows][S::kPad];
   __shared__ float s_self[S::kGroup][HD];
+  __shared__ int64_t s_now[kWarps][S::kGroup];   // the rows' times, a copy a warp
   // P of a warp's step, a row per column of the operand
   __shared__ __align__(16) uint16_t s_p[kWarps][S::kColumns][S::kStep + 8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -795,7 +805,6 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   uint32_t qb[QT][KS][2];
   // e4m3: the rows' scales of q, and what keeps their P within fp16
   float q_scale[S::kGroup], inv[S::kGroup], acc[MT][NT][4];
-  int64_t row0 = 0, now0 = 0;
   int nq = 1, folds = 0, chain = 0;
   fill_time(a, s_time, tid);
   bool up = sync(), done = false;
@@ -816,8 +825,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       // ---- a new part: q, and nothing summed; its pages are on their way
       const Part& p = ring.unit[st].part;
       nq = p.nq;
-      row0 = p.row0;
-      now0 = __ldg(a.ts + row0);
+      const int64_t row0 = p.row0;
+      __syncwarp();
+      if (lane < S::kGroup) s_now[warp][lane] = __ldg(a.ts + row0 + (lane < nq ? lane : nq - 1));
       // Columns 2i and 2i + 1 of the score product are query i, with the even and the odd
       // pairs of its dimensions: what the lane's g is, at its t's dimensions.
 #pragma unroll
@@ -925,6 +935,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           for (int i = 0; i < QT; ++i) s[nb][x][i] = c[i][0] + c[i][3];
         }
       }
+      const float pos = j0 + S::kStep > n - a.pos_clamp ? pos_bias(a, pos_far, n, jl) : pos_far;
       // ---- a lane a key: N rows of q at once, from row 4i on (those behind nq are copies of
       // the last, in columns that nobody reads)
       auto score = [&](auto count, int i) {
@@ -943,9 +954,26 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
             y[c] = lane & 16 ? z : y[c];
           }
           if constexpr (S::kF16) y[c] = y[c] * q_scale[4 * i + c] * ks;
-          int64_t now = now0;
-          if (4 * i + c > 0) now = __ldg(a.ts + row0 + (4 * i + c < nq ? 4 * i + c : nq - 1));
-          y[c] = silu(y[c] + bias_of(a, s_time, pos_far, n, jl, now, then));
+        }
+        // lanes without a key take gap 0
+        int64_t gap[N];
+        bool bins = true;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          gap[c] = mine ? gap_of(s_now[warp][4 * i + c], then) : 0;
+          bins = bins && bin_gap(a, gap[c]);
+        }
+        float tb[N];
+        if (__all_sync(0xffffffffu, bins)) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) tb[c] = bin_bias(s_time, uint32_t(gap[c]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < N; ++c) tb[c] = time_bias(a, s_time, gap[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          y[c] = silu(y[c] + (pos + tb[c]));
           if constexpr (S::kF16) y[c] *= vs;
           y[c] = mine ? y[c] : 0.f;      // no key here: what memory holds must not reach the sum
         }
