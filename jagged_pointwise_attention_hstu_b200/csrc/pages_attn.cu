@@ -94,16 +94,23 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// What a variant of the kernel is made of.  NT: tiles of 8 columns of P.
+// What a variant of the kernel is made of.  NT: tiles of 8 columns of P (fp32 pages: rows).
+// Row 4i + t of q has its pieces in columns that lane t of a quad holds: 0 and 1 in tile i at
+// 2t and 2t + 1; a third one in tile 2 at 2t + i, or, with one tile for two rows, at
+// 2t + 4, which is two lanes on.
 template <int FMT, int HD, int NT>
 struct Shape {
   static constexpr bool kF32 = FMT == HSTU_PAGES_FP32;
   static constexpr bool kF16 = FMT == HSTU_PAGES_E4M3;
   static constexpr int kPieces = kF32 ? 1 : (kF16 ? 2 : 3);
-  static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 2 * NT);   // rows of q of a segment
+  static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 8 * NT / 3);   // rows of q of a segment
   static constexpr int kTiles = (kGroup + 3) / 4;               // of 4 rows of q, for the scores
   static constexpr int kColumns = 8 * NT;                       // of P
-  static constexpr int kRows = kF32 ? 4 : kGroup * kPieces;     // of the sums
+  static constexpr int kRows = kF32 ? 4 : kGroup;               // of the sums
+  static __device__ __forceinline__ int column(int row, int piece) {
+    if (piece < 2) return 2 * row + piece;
+    return NT == 1 ? 4 + 2 * row : 16 + 2 * (row & 3) + (row >> 2);
+  }
   static constexpr int kRow = HD * (kF32 ? 4 : (kF16 ? 1 : 2)); // bytes of a key
   static constexpr int kBlocks = !kF32 && kRow == 64 ? 2 : 1;            // of 16 keys, a warp's step
   static constexpr int kStep = 16 * kBlocks;                    // keys of a warp's step
@@ -117,7 +124,7 @@ struct Shape {
   static constexpr int kSideBytes = 8 * kUnit + (kF16 ? 2 * kUnit : 0);
   static constexpr int kRingBytes(int stages) { return stages * (kDataBytes + kSideBytes); }
   static constexpr int kStages = kRow == 256 || kUnit * kRow > 8192 ? 2 : 3;
-  static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT == 2 ? 2 : 3);
+  static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT > 1 ? 2 : 3);
 };
 
 struct User {
@@ -407,9 +414,7 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, Sum& s
     const int q = i / HD, c = i % HD;
     float x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-#pragma unroll
-      for (int k = 0; k < S::kPieces; ++k) x += sum[w][q * S::kPieces + k][c];
+    for (int w = 0; w < kWarps; ++w) x += sum[w][q][c];
     if (p.tile0 == 0) x += self[q][c];
     if (whole) a.av[(p.row0 + q) * a.d + p.h * HD + c] = x / float(a.n_norm);
     else part[i] = x;
@@ -1006,8 +1011,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
             const __half hi = __float2half_rn(y[c]);
             const __half lo = __float2half_rn(y[c] - __half2float(hi));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[8 * i + 2 * c][spot] = __half_as_ushort(hi);
-              ps[8 * i + 2 * c + 1][spot] = __half_as_ushort(lo);
+              ps[S::column(4 * i + c, 0)][spot] = __half_as_ushort(hi);
+              ps[S::column(4 * i + c, 1)][spot] = __half_as_ushort(lo);
             }
           }
         } else {
@@ -1018,9 +1023,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
             const __nv_bfloat16 mid = __float2bfloat16_rn(y[c]);
             const __nv_bfloat16 lo = __float2bfloat16_rn(y[c] - __bfloat162float(mid));
             if (S::kStep == 32 || lane < S::kStep) {
-              ps[3 * c][spot] = __bfloat16_as_ushort(hi);
-              ps[3 * c + 1][spot] = __bfloat16_as_ushort(mid);
-              ps[3 * c + 2][spot] = __bfloat16_as_ushort(lo);
+              ps[S::column(4 * i + c, 0)][spot] = __bfloat16_as_ushort(hi);
+              ps[S::column(4 * i + c, 1)][spot] = __bfloat16_as_ushort(mid);
+              ps[S::column(4 * i + c, 2)][spot] = __bfloat16_as_ushort(lo);
             }
           }
         }
@@ -1085,30 +1090,38 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     ++chain;
     if (chain == kFold || (what.z & kLast)) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        float scale = 1.f;                         // of row t of the tile
+      for (int i = 0; i < QT; ++i) {
+        float scale = 1.f;                         // of row 4i + t
         if constexpr (S::kF16) {
           const float f01 = t & 1 ? inv[4 * i + 1] : inv[4 * i], f23 = t & 1 ? inv[4 * i + 3] : inv[4 * i + 2];
           scale = 1.f / (t & 2 ? f23 : f01);
         }
-        const int r = 8 * i + 2 * t;
-        if (r >= S::kRows) continue;               // columns without a row of q
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const int dim = (S::kF16 ? g * (HD / 8) + 2 * m : 64 * (m >> 2) + 8 * g + 2 * (m & 3));
-          float2* p0 = reinterpret_cast<float2*>(&sum[r][dim]);
-          float2* p1 = reinterpret_cast<float2*>(&sum[r + 1][dim]);
-          float2 x0 = make_float2(acc[m][i][0] * scale, acc[m][i][2] * scale);
-          float2 x1 = make_float2(acc[m][i][1] * scale, acc[m][i][3] * scale);
-          if (folds > 0) {
-            const float2 y0 = *p0, y1 = *p1;
-            x0.x += y0.x, x0.y += y0.y, x1.x += y1.x, x1.y += y1.y;
+          float2 x = make_float2(acc[m][i][0] + acc[m][i][1], acc[m][i][2] + acc[m][i][3]);
+          if constexpr (S::kF16) {
+            x.x *= scale, x.y *= scale;
+          } else if constexpr (NT > 1) {
+            x.x += acc[m][2][i], x.y += acc[m][2][2 + i];
+          } else {
+            x.x += __shfl_xor_sync(0xffffffffu, acc[m][0][0], 2);
+            x.y += __shfl_xor_sync(0xffffffffu, acc[m][0][2], 2);
           }
-          *p0 = x0;
-          *p1 = x1;
-          acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+          if (4 * i + t < S::kGroup) {
+            float2* at = reinterpret_cast<float2*>(&sum[4 * i + t][dim]);
+            if (folds > 0) {
+              const float2 y = *at;
+              x.x += y.x, x.y += y.y;
+            }
+            *at = x;
+          }
         }
       }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
       ++folds;
       chain = 0;
     }
@@ -1142,6 +1155,7 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
   static_assert(S::kPerSm <= kPagesBlocksPerSm, "workspace");
   static_assert(S::kGroup * HD <= kPagesPartial && S::kGroup <= 8, "workspace");
   static_assert(S::kTiles * 4 >= S::kGroup && S::kGroup * S::kPieces <= S::kColumns, "operand");
+  static_assert(S::kF32 || NT == 1 || NT == (FMT == HSTU_PAGES_BF16 ? 3 : 2), "columns");
   static_assert(S::kHalves * 128 >= S::kRow || !S::kSwizzle, "boxes");
   static_assert(S::kF32 || S::kRingBytes(S::kStages) <= 128 * 1024, "ring");
   if constexpr (S::kF32) {
@@ -1172,7 +1186,8 @@ cudaError_t launch_pages_attention(const PagesArgs& a, cudaStream_t st) {
   if (a.R <= 0 || a.B <= 0) return cudaSuccess;
   // more rows than users: candidates, so the variants that take more rows of a user at once
   const bool wide = a.R > a.B;
-#define HSTU_PAGES_ATTN(F, D) return wide ? launch<F, D, 2>(a, st) : launch<F, D, 1>(a, st)
+#define HSTU_PAGES_ATTN(F, D) \
+  return wide ? launch<F, D, (F == HSTU_PAGES_BF16 ? 3 : 2)>(a, st) : launch<F, D, 1>(a, st)
   if (a.format == HSTU_PAGES_FP32) {
     switch (a.hd) {
       case 32: HSTU_PAGES_ATTN(HSTU_PAGES_FP32, 32);

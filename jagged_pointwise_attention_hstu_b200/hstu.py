@@ -177,19 +177,17 @@ def _check(status: int, what: str) -> None:
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:   # an address, or None
         return t
-    return t.data_ptr()
 
 
 def _stream_ptr(stream) -> Optional[int]:
-    if stream is None:
-        return None
-    if isinstance(stream, int):
+    try:
+        return stream.cuda_stream
+    except AttributeError:   # a cudaStream_t, or None
         return stream
-    return stream.cuda_stream
 
 
 # ----------------------------------------------------------------- entry points
