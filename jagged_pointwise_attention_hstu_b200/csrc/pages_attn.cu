@@ -153,13 +153,14 @@ __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err)
 //
 // Parts, if every block can have one part of one segment, of at most `share`
 // units: then it does, the segments cut into equal parts.  Else runs: block c has
-// the units from c * share on, whatever segments they belong to; but a segment at
-// most kJoin units longer than that is not cut, the block it begins in takes it
-// whole.  A cut costs the join of its parts (2 to 3 us: the parts' way to memory, a
-// ticket, the parts' way back), as much as a few units, and a block with the
-// ends of two segments pays for two.  (16 users of up to 4096 rows, d 512: runs
-// 15.9 us, parts 13.8; 1 of 100003: 32.9 and 30.7.)
-constexpr int kJoin = 4;
+// the units from c * share on, whatever segments they belong to; but a segment of
+// at most share / 8 units is not cut, the block it begins in takes it whole.  A cut
+// costs the join of its parts (2 to 3 us: the parts' way to memory, a ticket, the
+// parts' way back), as much as a few units, and a block with the ends of two
+// segments pays for two.  (16 users of up to 4096 rows, d 512: runs 15.9 us,
+// parts 13.8; 1 of 100003: 32.9 and 30.7.  Longer segments left whole put two on some
+// blocks and none on others: 109 users of up to 3698 rows, d 256, 39 us where
+// segments up to 4 units longer than the share were.)
 constexpr int32_t kWarpUsers = 64;   // with more users all threads plan, not one warp
 
 struct Plan {
@@ -252,7 +253,7 @@ __device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl) {
       const int32_t k = x.segments * pieces;
       if (u < at + k) {
         const int32_t rel = u - at;
-        const int32_t cut = x.nu <= share + kJoin ? u - rel % x.nu : u;
+        const int32_t cut = x.nu <= share / 8 ? u - rel % x.nu : u;
         if (end == 1) {
           pl.u1 = cut;
         } else {
@@ -430,32 +431,37 @@ __device__ __forceinline__ bool finish(const PagesArgs& a, const Part& p, Sum& s
     }
     if (!sync()) return false;
     if (*last) {
-      // A thread has four columns of every kSlots-th part (a segment over the whole GPU has
-      // hundreds of parts, and one after the other their latency was the call's); the slots
-      // are added in order, through the shared memory of the sums.
-      constexpr int kQuads = HD / 4, kSlots = kAll / kQuads;   // per row of the group
+      // A thread has four columns of a row in every slots-th part (a segment over the whole GPU
+      // has hundreds, and one after the other their latency was the call's); the slots are
+      // added in order, through the shared memory of the sums.
+      const int32_t quads = p.nq * (HD / 4), slots = quads < kAll ? kAll / quads : 1;
       float* all = &sum[0][0][0];
-      static_assert(sizeof(sum) >= size_t(kSlots) * HD * 4, "slots");
-      const int quad = tid % kQuads, slot = tid / kQuads;
-      for (int q = 0; q < p.nq; ++q) {
+      static_assert(sizeof(sum) >= size_t(kAll) * 16, "slots");
+      auto out = [&](int32_t i, float x) {
+        a.av[(p.row0 + i / HD) * a.d + p.h * HD + i % HD] = x / float(a.n_norm);
+      };
+      for (int32_t i = tid; i < quads * slots; i += slots > 1 ? kAll * 2 : kAll) {
+        const int32_t quad = i % quads;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (slot < kSlots) {
 #pragma unroll 4
-          for (int32_t c = p.c0 + slot; c <= p.c1; c += kSlots) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(
-                a.partial + (int64_t(c) * 2 + (c == p.c0 ? 1 : 0)) * (S::kGroup * HD) + q * HD) + quad);
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-          }
-          *reinterpret_cast<float4*>(all + slot * HD + 4 * quad) = x;
+        for (int32_t c = p.c0 + i / quads; c <= p.c1; c += slots) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(
+              a.partial + (int64_t(c) * 2 + (c == p.c0 ? 1 : 0)) * (S::kGroup * HD)) + quad);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        if (!sync()) return false;
-        for (int i = tid; i < HD; i += kAll) {
-          float y = 0.f;
-#pragma unroll
-          for (int k = 0; k < kSlots; ++k) y += all[k * HD + i];
-          a.av[(p.row0 + q) * a.d + p.h * HD + i] = y / float(a.n_norm);
+        if (slots > 1) {
+          *reinterpret_cast<float4*>(all + 4 * i) = x;
+        } else {
+          out(4 * quad, x.x), out(4 * quad + 1, x.y), out(4 * quad + 2, x.z), out(4 * quad + 3, x.w);
         }
+      }
+      if (slots > 1) {
         if (!sync()) return false;
+        for (int32_t i = tid; i < 4 * quads; i += kAll) {
+          float x = 0.f;
+          for (int32_t k = 0; k < slots; ++k) x += all[k * 4 * quads + i];
+          out(i, x);
+        }
       }
     }
   }
