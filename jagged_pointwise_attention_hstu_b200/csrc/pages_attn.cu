@@ -103,7 +103,8 @@ struct Shape {
   static constexpr bool kF32 = FMT == HSTU_PAGES_FP32;
   static constexpr bool kF16 = FMT == HSTU_PAGES_E4M3;
   static constexpr int kPieces = kF32 ? 1 : (kF16 ? 2 : 3);
-  static constexpr int kGroup = kF32 ? NT : (kF16 ? 4 * NT : 8 * NT / 3);   // rows of q of a segment
+  // rows of q of a segment (4 would fit a tile of e4m3 at head dim 128, but not three blocks an SM)
+  static constexpr int kGroup = kF32 ? NT : NT > 1 ? 8 : kF16 && HD == 64 ? 4 : 2;
   static constexpr int kTiles = (kGroup + 3) / 4;               // of 4 rows of q, for the scores
   static constexpr int kColumns = 8 * NT;                       // of P
   static constexpr int kRows = kF32 ? 4 : kGroup;               // of the sums
@@ -122,9 +123,14 @@ struct Shape {
   static constexpr int kHalves = kSwizzle ? kRow / 128 : 1;     // boxes of 128 bytes of a row
   static constexpr int kDataBytes = 2 * kUnit * kRow;
   static constexpr int kSideBytes = 8 * kUnit + (kF16 ? 2 * kUnit : 0);
-  static constexpr int kRingBytes(int stages) { return stages * (kDataBytes + kSideBytes); }
-  static constexpr int kStages = kRow == 256 || kUnit * kRow > 8192 ? 2 : 3;
-  static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : (kRow == 256 || NT > 1 ? 2 : 3);
+  static constexpr int kRowsBytes = 3 * kGroup * HD * 2;        // a part's q, k and v
+  static constexpr int kRingBytes(int stages) { return stages * (kDataBytes + kSideBytes + kRowsBytes); }
+  // blocks an SM and stages a block: as many blocks as registers allow, for parts that end at
+  // different times, and what is left for stages (bf16 at head dim 64: 4 blocks of 2 stages;
+  // 3 of 3 are 0 to 3 us slower)
+  static constexpr bool kBig = kRow == 256 || NT > 1;
+  static constexpr int kStages = kF16 && !kBig ? 3 : 2;
+  static constexpr int kPerSm = kF32 ? (HD == 128 ? 2 : 3) : kBig ? 2 : (kF16 ? 3 : 4);
 };
 
 struct User {
@@ -376,25 +382,18 @@ __device__ __forceinline__ int64_t gap_of(int64_t now, int64_t then) {
   return int64_t(uint64_t(now) - uint64_t(then));   // any two timestamps: no signed overflow
 }
 
-// What each row adds of itself, SiLU(s_r) v_r: a warp a row.
-template <class S, int HD, class Self>
-__device__ __forceinline__ void self_terms(const PagesArgs& a, const Part& p, float bias,
-                                           Self& self, int& err) {
+// What each row adds of itself, SiLU(s_r) v_r: a warp a row, its q, k and v by load(which, row,
+// dimension), which = 0, 1, 2.
+template <int HD, class Load, class Self>
+__device__ __forceinline__ void self_terms(int nq, float bias, Load load, Self& self) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int q = warp; q < p.nq; q += kWarps) {
-    const int64_t at = (p.row0 + q) * 4 * a.d + a.d + p.h * HD + lane;
-    auto load = [&](int64_t i) {
-      return S::kF32 ? static_cast<const float*>(a.uvqk)[i]
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(a.uvqk)[i]);
-    };
+  for (int q = warp; q < nq; q += kWarps) {
     float s = 0.f, v[HD / 32];
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e) {
-      v[e] = load(at + 32 * e);
-      s = fmaf(load(at + a.d + 32 * e), load(at + 2 * a.d + 32 * e), s);
+      v[e] = load(2, q, lane + 32 * e);
+      s = fmaf(load(0, q, lane + 32 * e), load(1, q, lane + 32 * e), s);
     }
-    const int64_t ts = __ldg(a.ts + p.row0 + q);
-    if (ts < 0 || ts >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
     s = silu(warp_sum(s) + bias);
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e) self[q][lane + 32 * e] = s * v[e];
@@ -496,13 +495,19 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   while (walk.next(a, p)) {
     const int32_t n = p.n;
     const int32_t* table = a.table + int64_t(p.b) * a.width;
-    if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
+    if (p.tile0 == 0) {
+      const float* rows = static_cast<const float*>(a.uvqk) + p.row0 * 4 * a.d + p.h * HD;
+      self_terms<HD>(p.nq, self_bias, [&](int which, int q, int c) {
+        return rows[(int64_t(q) * 4 + (which == 0 ? 2 : which == 1 ? 3 : 1)) * a.d + c];
+      }, s_self);
+    }
     float q[NT][4 * E], o[NT][4 * E];
     int64_t now[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int64_t r = p.row0 + (i < p.nq ? i : 0);
       now[i] = __ldg(a.ts + r);
+      if (now[i] < 0 || now[i] >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.uvqk) +
@@ -593,6 +598,7 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
 struct Unit {
   int4 what;             // tile, runs (below) whose page index is none, Flag, cached rows
   Part part;
+  int64_t now[8];        // of a part's first unit: the rows' times
 };
 enum Flag { kLast = 1, kStop = 2 };   // of its part; no more units
 
@@ -635,7 +641,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
 
 template <class S>
 struct Ring {
-  uint64_t head[S::kStages], full[S::kStages], empty[S::kStages], turn;
+  uint64_t full[S::kStages], empty[S::kStages], turn;
   Unit unit[S::kStages];
   int32_t last;
 };
@@ -666,7 +672,6 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   const long long limit = a.wait_limit > 0 ? a.wait_limit : kWaitLimit;
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&ring.head[s], 1);
       mbar_init(&ring.full[s], 1);
       mbar_init(&ring.empty[s], kWarps);
     }
@@ -696,6 +701,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         const int32_t x = __ldg(table + (j >> a.page_shift));
         return x >= 0 && x < a.num_pages ? x : -2;
       };
+      const int64_t now = lane < p.nq ? __ldg(a.ts + p.row0 + lane) : 0;
+      if (now < 0 || now >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
       int32_t page_next = page_of(p.tile0);
       for (int32_t tile = p.tile0; tile < p.tile1; ++tile) {
         const int32_t page = page_next;
@@ -709,16 +716,28 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         // whole blocks of 16 keys: what lies behind the history in the last one is not used
         int32_t keys = page >= 0 ? (p.n - j < run ? (p.n - j + 15) & ~15 : run) : 0;
         const uint32_t per_key = 2 * S::kRow + (S::kF16 ? 2 : 0) + 8;
-        const uint32_t bytes = __reduce_add_sync(0xffffffffu, uint32_t(keys) * per_key);
+        // with a part's first unit come its rows of q, and of k and v where it is a segment's first
+        const int32_t rows = tile == p.tile0 ? p.nq * (tile == 0 ? 3 : 1) : 0;
+        const uint32_t bytes = __reduce_add_sync(0xffffffffu, uint32_t(keys) * per_key +
+                                                                 (lane < rows ? HD * 2 : 0));
         const unsigned bad = __ballot_sync(0xffffffffu, page == -2);
         if (bad != 0) err |= HSTU_DEVERR_PAGES;
         if (lane == 0) {
           ring.unit[s].part = p;
           ring.unit[s].what = make_int4(tile, int(bad), tile + 1 == p.tile1 ? kLast : 0, p.n);
-          mbar_arrive(&ring.head[s]);
-          mbar_arrive_expect_tx(&ring.full[s], bytes);
         }
+        if (rows > 0 && lane < S::kGroup) ring.unit[s].now[lane] = now;
         __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&ring.full[s], bytes);
+        __syncwarp();
+        if (lane < rows) {
+          const int32_t which = lane / p.nq, q = lane - which * p.nq;
+          const char* from = static_cast<const char*>(a.uvqk) +
+              (((p.row0 + q) * 4 + (which == 0 ? 2 : which == 1 ? 3 : 1)) * a.d + p.h * HD) * 2;
+          bulk_load(smem_u32(stages) + S::kStages * (S::kDataBytes + S::kSideBytes) +
+                        s * S::kRowsBytes + (which * S::kGroup + q) * (HD * 2),
+                    from, HD * 2, &ring.full[s]);
+        }
         if (keys > 0) {
           uint64_t* bar = &ring.full[s];
           const uint32_t data = smem_u32(stages) + s * S::kDataBytes;
@@ -761,12 +780,13 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     if (ok) ok = wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
     if (ok && lane == 0) {
       ring.unit[s].what = make_int4(0, 0, kStop, 0);
-      mbar_arrive(&ring.head[s]);
+      mbar_arrive(&ring.full[s]);
     }
     if (!ok) err |= HSTU_DEVERR_TIMEOUT;
-    // no copy may land after the block has gone, whoever gave up
+    // no copy may land after the block has gone, whoever gave up (the stage of the stop has
+    // been given back: its copies have landed)
     for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0; k < issued; ++k)
-      mbar_wait(&ring.full[k % S::kStages], (k / S::kStages) & 1);
+      if (!ok || k % S::kStages != s) mbar_wait(&ring.full[k % S::kStages], (k / S::kStages) & 1);
     if (err != 0) atomicOr(a.error, err);
     return;
   }
@@ -777,6 +797,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   constexpr int KS = HD / 32;                  // products a tile of scores takes
   constexpr int MT = HD / 16;                  // tiles of 16 dimensions of the output
   constexpr int QT = S::kTiles;
+  constexpr int kQ = S::kGroup < 4 ? S::kGroup : 4;   // rows of a tile
   const int g = lane >> 2, t = lane & 3;
   const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
   const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
@@ -823,8 +844,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   bool fresh = true;                           // the next unit begins a part, or there is none
   uint32_t parity = 0;
   for (int st = 0; up;) {
-    if (fresh && __any_sync(0xffffffffu, !wait_for(&ring.head[st], parity, limit))) break;
-    if (!fresh && __any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
+    if (__any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
     const int4 what = ring.unit[st].what;
     if (what.z & kStop) {
       done = true;
@@ -833,24 +853,23 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     const int32_t tile = what.x, n = what.w;
 
     if (fresh) {
-      // ---- a new part: q, and nothing summed; its pages are on their way
-      const Part& p = ring.unit[st].part;
-      nq = p.nq;
-      const int64_t row0 = p.row0;
+      // ---- a new part: q, and nothing summed
+      const __nv_bfloat16* rows = reinterpret_cast<const __nv_bfloat16*>(
+          stages + S::kStages * (S::kDataBytes + S::kSideBytes) + st * S::kRowsBytes);
+      nq = ring.unit[st].part.nq;
       __syncwarp();
-      if (lane < S::kGroup) s_now[warp][lane] = __ldg(a.ts + row0 + (lane < nq ? lane : nq - 1));
+      if (lane < S::kGroup) s_now[warp][lane] = ring.unit[st].now[lane < nq ? lane : nq - 1];
       // Columns 2i and 2i + 1 of the score product are query i, with the even and the odd
       // pairs of its dimensions: what the lane's g is, at its t's dimensions.
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
         const int q = 4 * i + (g >> 1) < nq ? 4 * i + (g >> 1) : nq - 1;
         const bool odd = (g & 1) != 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(a.uvqk) + (row0 + q) * 4 * a.d + 2 * a.d + p.h * HD);
+        const uint4* src = reinterpret_cast<const uint4*>(rows + q * HD);
         if constexpr (!S::kF16) {
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
-            const uint4 v = __ldg(src + chunk(c));
+            const uint4 v = src[chunk(c)];
             qb[i][c][0] = odd ? v.y : v.x;
             qb[i][c][1] = odd ? v.w : v.z;
           }
@@ -861,8 +880,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           float m = 0.f;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
-            unpack_bf16(__ldg(src + 2 * chunk(c)), x[c]);
-            unpack_bf16(__ldg(src + 2 * chunk(c) + 1), x[c] + 8);
+            unpack_bf16(src[2 * chunk(c)], x[c]);
+            unpack_bf16(src[2 * chunk(c) + 1], x[c] + 8);
 #pragma unroll
             for (int y = 0; y < 16; ++y) m = fmaxf(m, fabsf(x[c][y]));
           }
@@ -872,7 +891,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
           e = e < -126 ? -126 : (e > 112 ? 112 : e);
           const float qs = __int_as_float((e + 127) << 23), f = __int_as_float((127 - e) << 23);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) q_scale[4 * i + c] = __shfl_sync(0xffffffffu, qs, 8 * c);
+          for (int c = 0; c < kQ; ++c) q_scale[4 * i + c] = __shfl_sync(0xffffffffu, qs, 8 * c);
 #pragma unroll
           for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -896,8 +915,10 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
 #pragma unroll
       for (int i = 0; i < S::kGroup; ++i) inv[i] = __int_as_float((127 + 126) << 23);
       folds = chain = 0;
-      if (p.tile0 == 0) self_terms<S, HD>(a, p, self_bias, s_self, err);
-      if (__any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
+      if (tile == 0)
+        self_terms<HD>(nq, self_bias, [&](int which, int q, int c) {
+          return __bfloat162float(rows[(which * S::kGroup + q) * HD + c]);
+        }, s_self);
     }
 
     const int32_t k0 = warp * S::kStep, j0 = tile * S::kUnit + k0;   // the warp's keys
@@ -1040,7 +1061,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
 #pragma unroll
       for (int i = 0; i < QT; ++i) {
         if (nq == 4 * i + 1) score(std::integral_constant<int, 1>{}, i);
-        else if (nq > 4 * i) score(std::integral_constant<int, (S::kGroup < 4 ? S::kGroup : 4)>{}, i);
+        else if (nq > 4 * i) score(std::integral_constant<int, kQ>{}, i);
       }
       __syncwarp();
 #pragma unroll
@@ -1099,8 +1120,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       for (int i = 0; i < QT; ++i) {
         float scale = 1.f;                         // of row 4i + t
         if constexpr (S::kF16) {
-          const float f01 = t & 1 ? inv[4 * i + 1] : inv[4 * i], f23 = t & 1 ? inv[4 * i + 3] : inv[4 * i + 2];
-          scale = 1.f / (t & 2 ? f23 : f01);
+          float f = t & 1 ? inv[4 * i + 1] : inv[4 * i];
+          if constexpr (kQ == 4) f = t & 2 ? (t & 1 ? inv[4 * i + 3] : inv[4 * i + 2]) : f;
+          scale = 1.f / f;
         }
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
