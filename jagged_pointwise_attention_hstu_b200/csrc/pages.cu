@@ -38,7 +38,7 @@ __device__ __forceinline__ int32_t user_of_row(const int32_t* __restrict__ offs,
   while (n > 1) {
     const int32_t step = (n + 31) >> 5;
     const int32_t k = lane * step;
-    const bool le = k < n && int64_t(__ldg(offs + lo + k)) <= r;
+    const bool le = k < n && __ldg(offs + lo + k) <= r;
     const unsigned m = __ballot_sync(0xffffffffu, le);
     const int32_t top = m == 0 ? 0 : 31 - __clz(m);
     lo += top * step;
@@ -47,9 +47,9 @@ __device__ __forceinline__ int32_t user_of_row(const int32_t* __restrict__ offs,
   return lo;
 }
 
-struct Place {
-  int64_t row;   // (page * H) * 2 * page_size + slot: the block of plane 0 of head 0
-  int64_t ts;    // index into the page timestamps
+struct Place {         // 32 bits: a pool has fewer rows than 2^31
+  int32_t row;         // (page * H) * 2 * page_size + slot: the block of plane 0 of head 0
+  int32_t ts;          // index into the page timestamps
   int err;
   bool ok;
 };
@@ -68,36 +68,28 @@ __device__ __forceinline__ void check_offsets(const PagesArgs& a) {
 
 // Where row r of the call lives, by the whole warp; `ok` false: nowhere (a row
 // behind the last sequence, or an error).
-__device__ __forceinline__ Place place_of(const PagesArgs& a, int64_t r, int lane) {
+__device__ __forceinline__ Place place_of(const PagesArgs& a, int32_t r, int lane) {
   Place p;
   p.ok = false;
   p.err = 0;
   p.row = 0;
   p.ts = 0;
   const int32_t b = user_of_row(a.offsets, a.B, r, lane);
-  const int64_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
-  if (r < r0 || r >= r1 || r0 < 0 || r1 > a.R) {
-    // behind the last sequence, or a table that check_offsets reports
-    return p;
-  }
-  if (a.one_row && r1 - r0 > 1) {
-    p.err = HSTU_DEVERR_PAGES;
-    return p;
-  }
-  // a length is an int32, and the rows of a user fewer than 2^30: no overflow past int64
-  const int64_t pos = (a.lengths != nullptr ? int64_t(__ldg(a.lengths + b)) : 0) + (r - r0);
-  if (pos < 0 || (pos >> a.page_shift) >= a.width) {
-    p.err = HSTU_DEVERR_PAGES;
-    return p;
-  }
-  const int32_t page = __ldg(a.table + (int64_t(b) * a.width + (pos >> a.page_shift)));
-  if (page < 0 || page >= a.num_pages) {
-    p.err = HSTU_DEVERR_PAGES;
-    return p;
-  }
-  const int32_t slot = int32_t(pos & ((1 << a.page_shift) - 1));
-  p.row = ((int64_t(page) * a.H * 2) << a.page_shift) + slot;
-  p.ts = (int64_t(page) << a.page_shift) + slot;
+  const int32_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
+  // behind the last sequence, or a table that check_offsets reports
+  if (r < r0 || r >= r1 || r0 < 0 || r1 > a.R) return p;
+  p.err = HSTU_DEVERR_PAGES;
+  if (a.one_row && r1 - r0 > 1) return p;
+  const int32_t first = a.lengths != nullptr ? __ldg(a.lengths + b) : 0;
+  if (first < 0 || first >= (1 << 30)) return p;       // positions end at 2^30, rows too
+  const int32_t pos = first + (r - r0), k = pos >> a.page_shift;
+  if (k >= int32_t(a.width)) return p;
+  const int32_t page = __ldg(a.table + (int64_t(b) * int32_t(a.width) + k));
+  if (page < 0 || page >= a.num_pages) return p;
+  const int32_t slot = pos & ((1 << a.page_shift) - 1);
+  p.row = ((page * a.H * 2) << a.page_shift) + slot;
+  p.ts = (page << a.page_shift) + slot;
+  p.err = 0;
   p.ok = true;
   return p;
 }
@@ -120,6 +112,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t times2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // Codes of a lane's eight bf16 of a block that kLanes neighbouring lanes hold,
 // and the block's scale byte; by the whole warp.
 //
@@ -133,18 +131,20 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, int& scale) {
 #pragma unroll
   for (int o = kLanes >> 1; o > 0; o >>= 1) top = max2(top, __shfl_xor_sync(0xffffffffu, top, o));
   top = max(top & 0xffffu, top >> 16);
-  float x[8];
-  unpack_bf16(v, x);
   uint2 c;
   if (!__any_sync(0xffffffffu, top > 0x7F60u)) {
     // e + 127 with e = k - 8 for top in (1.75 * 2^(k - 1), 1.75 * 2^k]: 0x1F carries above it
     scale = max(int((top + 0x1Fu) >> 7) - 8, kMinExponent + 127);
     scale = top == 0 ? 127 : scale;
-    const float inv = __int_as_float((254 - scale) << 23);
-    c.x = four_codes(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    c.y = four_codes(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+    // x * 2^-e in bf16: exact, or so small that its code is zero either way
+    const uint32_t inv = uint32_t(254 - scale) * 0x00800080u;
+    float x[8];
+    unpack_bf16(make_uint4(times2(v.x, inv), times2(v.y, inv), times2(v.z, inv), times2(v.w, inv)), x);
+    c.x = four_codes(x[0], x[1], x[2], x[3]);
+    c.y = four_codes(x[4], x[5], x[6], x[7]);
   } else {
-    float m = 0.f;
+    float x[8], m = 0.f;
+    unpack_bf16(v, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
 #pragma unroll
@@ -161,86 +161,114 @@ __device__ __forceinline__ uint2 quantise8(const uint4& v, int& scale) {
   return c;
 }
 
-// A row's keys and values in chunks of 16 bytes, heads of the keys first: lane
-// `lane` has the chunks lane, lane + 32, ..., which are the same place of a
-// block's kPerHead whatever the block (96, fp32 only: heads of 24 chunks).
+// A row's keys, and its values, in chunks of 16 bytes: lane `lane` has the chunks lane,
+// lane + 32, ... of both, which are the same place of a block's kPerHead whatever the
+// block (but for heads of 96, fp32 only, of 24 chunks).
 template <int FMT, int HD>
 struct Chunks {
   static constexpr int kElems = FMT == HSTU_PAGES_FP32 ? 4 : 8;   // elements of a chunk
   static constexpr int kPerHead = HD / kElems;
-  static constexpr int kBatch = 4;                                // of a lane, loaded at once
-  int lane, H, shift;
-  __device__ __forceinline__ Chunks(const PagesArgs& a)
-      : lane(threadIdx.x & 31), H(a.H), shift(a.page_shift) {}
-  __device__ __forceinline__ int all() const { return 2 * H * kPerHead; }
-  // of U | V | Q | K: K (the first half), then V
-  __device__ __forceinline__ int column(int c) const { return c + (c < H * kPerHead ? 3 * H * kPerHead : 0); }
+  static constexpr int kBatch = 4;                                // of each, loaded at once
+  int lane, each, step;     // chunks of the keys; blocks from a head to the next
+  __device__ __forceinline__ explicit Chunks(const PagesArgs& a)
+      : lane(threadIdx.x & 31), each(a.H * kPerHead), step(2 << a.page_shift) {}
+  // chunk c of the keys, from the row's first block: its block, and its place there
+  __device__ __forceinline__ int block(int c) const { return c / kPerHead * step; }
   __device__ __forceinline__ int in(int c) const {
     return 32 % kPerHead == 0 ? lane % kPerHead : c % kPerHead;
-  }
-  // of the block, from the row's first: head h's keys are block 2h, its values 2h + 1
-  __device__ __forceinline__ int block(int c) const {
-    const int b = c / kPerHead;
-    return (2 * b - (b < H ? 0 : 2 * H - 1)) << shift;
   }
 };
 
 // One warp per row, a lane a chunk, straight into the row's blocks.  Bound by
-// memory: a row reads 2d elements and writes them (or their codes) once.  All
-// of a lane's loads (d 1024: 8) are on their way before the row's place is
-// looked up.  What it took to get there were fewer instructions, about 75 a
-// chunk of e4m3 (65536 rows of d 1024: 137 us at 205).
+// memory, a row reads 2d elements and writes them (or their codes) once, and nearly
+// by its instructions.  All of a lane's loads (d 1024: 8) are on their way
+// before the row's place is looked up; the scale bytes of a block's eight rows
+// are gathered and stored as one where they are neighbours, since a store of one
+// byte costs as much as one of 32 (65536 rows of d 1024 to e4m3 pages: 80 us with
+// 20 instructions a value more and a store a byte, 149 with one load at a time).
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const PagesArgs a) {
   using C = Chunks<FMT, HD>;
+  constexpr bool kScaled = FMT == HSTU_PAGES_E4M3;
+  static_assert(kRowWarps == 8, "scales of a block's rows are eight bytes");
+  __shared__ __align__(8) uint8_t s_scale[kScaled ? 32 : 1][kRowWarps];   // at most 16 heads
+  __shared__ int32_t s_row[kRowWarps];
   check_offsets(a);
-  const int64_t r = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  if (r >= a.R) return;
+  const int warp = threadIdx.x >> 5;
+  const int32_t r = int32_t(blockIdx.x) * kRowWarps + warp;   // fewer than 2^30
   const C ch(a);
-  const int all = ch.all();
-  const uint4* src = static_cast<const uint4*>(a.uvqk) + r * (2 * all);
-  uint4 v[C::kBatch];
+  const int lane = ch.lane, plane = 1 << a.page_shift;
+  // U | V | Q | K
+  const uint4* vals = static_cast<const uint4*>(a.uvqk) + (int64_t(r) * 4 + 1) * ch.each;
+  const uint4* keys = vals + 2 * ch.each;
+  uint4 v[2][C::kBatch];
   auto load = [&](int c0) {
 #pragma unroll
     for (int i = 0; i < C::kBatch; ++i) {
-      const int c = c0 + 32 * i + ch.lane;
-      v[i] = c < all ? __ldg(src + ch.column(c)) : make_uint4(0u, 0u, 0u, 0u);
+      const int c = c0 + 32 * i + lane;
+      const bool on = r < a.R && c < ch.each;
+      v[0][i] = on ? __ldg(keys + c) : make_uint4(0u, 0u, 0u, 0u);
+      v[1][i] = on ? __ldg(vals + c) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   load(0);
-  const Place p = place_of(a, r, ch.lane);
-  if (!p.ok) {
-    if (p.err != 0 && ch.lane == 0) atomicOr(a.error, p.err);
-    return;
+  Place p;
+  p.ok = false;
+  if (r < a.R) {
+    p = place_of(a, r, lane);
+    if (p.err != 0 && lane == 0) atomicOr(a.error, p.err);
   }
-  if (ch.lane == 0 && a.ts != nullptr) {
-    const int64_t t = a.ts[r];
-    if (t < 0 || t >= kMaxTimestamp) atomicOr(a.error, HSTU_DEVERR_TIMESTAMPS);
-    a.page_ts[p.ts] = t;
-  }
-  uint4* to = static_cast<uint4*>(a.kv) + p.row * C::kPerHead;
-  uint2* codes = static_cast<uint2*>(a.kv) + p.row * C::kPerHead;
-  uint8_t* scales = a.scales + p.row;
-  for (int c0 = 0;;) {
+  if (p.ok) {
+    if (lane == 0 && a.ts != nullptr) {
+      const int64_t t = a.ts[r];
+      if (t < 0 || t >= kMaxTimestamp) atomicOr(a.error, HSTU_DEVERR_TIMESTAMPS);
+      a.page_ts[p.ts] = t;
+    }
+    uint4* to = static_cast<uint4*>(a.kv) + int64_t(p.row) * C::kPerHead;
+    uint2* codes = static_cast<uint2*>(a.kv) + int64_t(p.row) * C::kPerHead;
+    for (int c0 = 0;;) {
 #pragma unroll
-    for (int i = 0; i < C::kBatch; ++i) {
-      if (c0 + 32 * i >= all) break;
-      const int c = c0 + 32 * i + ch.lane;
-      const int block = ch.block(c), in = ch.in(c);
-      if constexpr (FMT != HSTU_PAGES_E4M3) {
-        if (c < all) to[block * C::kPerHead + in] = v[i];
-      } else {
-        int scale;
-        const uint2 q = quantise8<C::kPerHead>(v[i], scale);
-        if (c < all) {
-          codes[block * C::kPerHead + in] = q;
-          if (in == 0) scales[block] = uint8_t(scale);
+      for (int i = 0; i < C::kBatch; ++i) {
+        if (c0 + 32 * i >= ch.each) break;
+        const int c = c0 + 32 * i + lane;
+        const bool on = c < ch.each;
+        const int at = ch.block(c) * C::kPerHead + ch.in(c);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {                 // keys, values
+          if constexpr (!kScaled) {
+            if (on) to[at + x * plane * C::kPerHead] = v[x][i];
+          } else {
+            int scale;
+            const uint2 q = quantise8<C::kPerHead>(v[x][i], scale);
+            if (on) {
+              codes[at + x * plane * C::kPerHead] = q;
+              if (ch.in(c) == 0) s_scale[2 * (c / C::kPerHead) + x][warp] = uint8_t(scale);
+            }
+          }
         }
       }
+      c0 += 32 * C::kBatch;
+      if (c0 >= ch.each) break;
+      load(c0);
     }
-    c0 += 32 * C::kBatch;
-    if (c0 >= all) break;
-    load(c0);
+  }
+  if constexpr (kScaled) {
+    if (lane == 0) s_row[warp] = p.ok ? p.row : -1;
+    __syncthreads();
+    const int b = threadIdx.x;                        // a thread a block
+    if (b < 2 * a.H) {
+      const int32_t row = s_row[0];
+      bool together = row >= 0 && row % kRowWarps == 0;
+#pragma unroll
+      for (int i = 1; i < kRowWarps; ++i) together = together && s_row[i] == row + i;
+      uint8_t* to = a.scales + (int64_t(b) << a.page_shift);
+      if (together) {
+        *reinterpret_cast<uint2*>(to + row) = *reinterpret_cast<const uint2*>(s_scale[b]);
+      } else {
+        for (int i = 0; i < kRowWarps; ++i)
+          if (s_row[i] >= 0) to[s_row[i]] = s_scale[b][i];
+      }
+    }
   }
 }
 
@@ -249,54 +277,61 @@ template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesArgs a) {
   using C = Chunks<FMT, HD>;
   check_offsets(a);
-  const int64_t r = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int32_t r = int32_t(blockIdx.x) * kRowWarps + int32_t(threadIdx.x >> 5);   // fewer than 2^30
   if (r >= a.R) return;
   const C ch(a);
-  const int all = ch.all();
-  const Place p = place_of(a, r, ch.lane);
+  const int lane = ch.lane, plane = 1 << a.page_shift;
+  const Place p = place_of(a, r, lane);
   if (!p.ok) {
-    if (p.err != 0 && ch.lane == 0) atomicOr(a.error, p.err);
+    if (p.err != 0 && lane == 0) atomicOr(a.error, p.err);
     return;
   }
-  uint4* dst = static_cast<uint4*>(a.out) + r * (2 * all);
-  const uint4* from = static_cast<const uint4*>(a.kv) + p.row * C::kPerHead;
-  const uint2* codes = static_cast<const uint2*>(a.kv) + p.row * C::kPerHead;
+  uint4* vals = static_cast<uint4*>(a.out) + (int64_t(r) * 4 + 1) * ch.each;
+  uint4* keys = vals + 2 * ch.each;
+  const uint4* from = static_cast<const uint4*>(a.kv) + int64_t(p.row) * C::kPerHead;
+  const uint2* codes = static_cast<const uint2*>(a.kv) + int64_t(p.row) * C::kPerHead;
   const uint8_t* scales = a.scales + p.row;
-  if (ch.lane == 0 && a.ts_out != nullptr) a.ts_out[r] = a.page_ts[p.ts];
-  for (int c0 = ch.lane; c0 < all; c0 += 32 * C::kBatch) {
-    uint4 v[C::kBatch];
-    float s[C::kBatch];
+  if (lane == 0 && a.ts_out != nullptr) a.ts_out[r] = a.page_ts[p.ts];
+  for (int c0 = lane; c0 < ch.each; c0 += 32 * C::kBatch) {
+    uint4 v[2][C::kBatch];
+    float s[2][C::kBatch];
 #pragma unroll
     for (int i = 0; i < C::kBatch; ++i) {
       const int c = c0 + 32 * i;
-      if (c >= all) continue;
+      if (c >= ch.each) continue;
       const int block = ch.block(c), at = block * C::kPerHead + ch.in(c);
-      if constexpr (FMT != HSTU_PAGES_E4M3) {
-        v[i] = __ldg(from + at);
-      } else {
-        const uint2 q = __ldg(codes + at);
-        v[i].x = q.x;
-        v[i].y = q.y;
-        s[i] = block_scale(__ldg(scales + block));
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (FMT != HSTU_PAGES_E4M3) {
+          v[x][i] = __ldg(from + at + x * plane * C::kPerHead);
+        } else {
+          const uint2 q = __ldg(codes + at + x * plane * C::kPerHead);
+          v[x][i].x = q.x;
+          v[x][i].y = q.y;
+          s[x][i] = block_scale(__ldg(scales + block + x * plane));
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < C::kBatch; ++i) {
       const int c = c0 + 32 * i;
-      if (c >= all) continue;
-      if constexpr (FMT == HSTU_PAGES_E4M3) {
-        float x[8];
-        unpack_e4m3(v[i].x, x);
-        unpack_e4m3(v[i].y, x + 4);
-        uint32_t w[4];
+      if (c >= ch.each) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {   // exact: 4 significant bits
-          const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * e] * s[i], x[2 * e + 1] * s[i]);
-          w[e] = *reinterpret_cast<const uint32_t*>(&t);
+      for (int x = 0; x < 2; ++x) {
+        if constexpr (FMT == HSTU_PAGES_E4M3) {
+          float f[8];
+          unpack_e4m3(v[x][i].x, f);
+          unpack_e4m3(v[x][i].y, f + 4);
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {   // exact: 4 significant bits
+            const __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * e] * s[x][i], f[2 * e + 1] * s[x][i]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&t);
+          }
+          v[x][i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        (x == 0 ? keys : vals)[c] = v[x][i];
       }
-      dst[ch.column(c)] = v[i];
     }
   }
 }
