@@ -97,7 +97,7 @@ hstu_status hstu_pages_read(hstu_handle* h, const hstu_page_pool* pool, const in
  *   rab_pos, rab_time   as in hstu_layer_weights
  *   av           device fp32 [R, d]
  * Needs a fixed n_norm (> 0), as the history cache does, and
- * R * num_heads * (table_width * page_size / 64 + 1) < 2^31; else HSTU_ERR_UNSUPPORTED. */
+ * R * num_heads * (table_width * page_size / 64 + 1) <= 2^30; else HSTU_ERR_UNSUPPORTED. */
 hstu_status hstu_pages_attention(hstu_handle* h, const hstu_page_pool* pool, const void* uvqk,
                                  int64_t total_rows, const int32_t* seq_offsets,
                                  int32_t num_users, const int64_t* timestamps,

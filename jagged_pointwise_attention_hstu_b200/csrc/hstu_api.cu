@@ -1469,7 +1469,7 @@ hstu_status check_page_rows(const hstu_handle* h, int64_t R, const int32_t* offs
 // The attention's pieces of work (64 keys at least, of one head and row) are counted in 32 bits.
 bool attention_fits(const hstu_handle* h, int64_t R, int32_t width, int32_t page_size) {
   const int64_t keys = int64_t(width) * page_size / 64 + 1;
-  return R <= INT32_MAX / (keys * h->cfg.num_heads);
+  return R <= (int64_t(1) << 30) / (keys * h->cfg.num_heads);
 }
 
 hstu_status check_ptrs(std::initializer_list<const void*> ps) {

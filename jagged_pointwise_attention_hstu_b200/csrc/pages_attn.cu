@@ -113,7 +113,9 @@ struct Shape {
     return NT == 1 ? 4 + 2 * row : 16 + 2 * (row & 3) + (row >> 2);
   }
   static constexpr int kRow = HD * (kF32 ? 4 : (kF16 ? 1 : 2)); // bytes of a key
-  static constexpr int kBlocks = !kF32 && kRow == 64 ? 2 : 1;            // of 16 keys, a warp's step
+  // blocks of 16 keys, a warp's step: two where a step of one would be 2 KB, and for several
+  // rows of q, whose work a lane a key is
+  static constexpr int kBlocks = !kF32 && (kRow == 64 || (kRow == 128 && NT > 1)) ? 2 : 1;
   static constexpr int kStep = 16 * kBlocks;                    // keys of a warp's step
   static constexpr int kUnit = kWarps * kStep;                  // keys of a unit
   static constexpr int kPad = HD + 8;                           // row stride of the sums
