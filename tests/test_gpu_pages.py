@@ -486,3 +486,140 @@ def test_an_expired_wait_is_reported_and_the_handle_recovers(fmt, d, H):
         assert torch.equal(_attend(h, pool, uvqk, counts, lens, ts, rp, rt), ref)
     assert h.device_error() == 0
     h.close()
+
+
+@pytest.mark.parametrize("fmt,d,H,counts", [
+    ("bf16", 256, 4, [5, 0, 0, 3, 0, 0, 0, 1, 0, 0]),      # fewer rows than users: small groups
+    ("e4m3", 1024, 8, [7, 0, 0, 1, 0, 0, 0, 1, 0, 0]),
+    ("bf16", 1024, 8, [9, 1, 1, 1, 1, 1, 8, 17, 1, 2]),    # more: groups of eight
+    ("e4m3", 512, 8, [9, 1, 1, 1, 1, 1, 8, 17, 1, 2]),
+    ("e4m3", 256, 2, [9, 1, 1, 1, 1, 1, 8, 17, 1, 2])])
+def test_rows_of_a_user_in_groups_of_every_size(fmt, d, H, counts):
+    lens, ps = [130, 40, 0, 333, 64, 1, 700, 95, 16, 17], 32
+    h = _handle(d, H, fmt)
+    pool = _filled(h, d, H, fmt, ps, lens, seed=40)
+    uvqk, ts = _query(d, fmt, counts, seed=41)
+    rp, rt = _tables(128, 128, seed=42)
+    av = _attend(h, pool, uvqk, counts, lens, ts, rp, rt)
+    torch.cuda.synchronize()
+    assert h.device_error() == 0
+    _check(av, pool, uvqk, counts, lens, ts, rp, rt, oracle_cfg(d, H, n_norm=N_NORM))
+    # a row's result is its own: one user's rows in calls of their own, another grouping
+    big = int(np.argmax(counts))
+    at = sum(counts[:big])
+    for i in (0, counts[big] - 1):
+        one = [0] * len(counts)
+        one[big] = 1
+        got = _attend(h, pool, uvqk[at + i:at + i + 1].contiguous(), one, lens, ts[at + i:at + i + 1].clone(),
+                      rp, rt)
+        n = lens[big]
+        k, v, kt = pool.rows(big, n)
+        x = uvqk[at + i].double().cpu().numpy().reshape(1, 4, H, d // H)
+        _, big_a, big_s = ph.paged_attention(
+            x[:, 2], x[:, 3], x[:, 1], ts[at + i:at + i + 1].cpu().numpy(), k, v, kt,
+            rp.double().cpu().numpy(), rt.double().cpu().numpy(),
+            oracle_cfg(d, H, n_norm=N_NORM), with_scale=True)
+        tol = 2 * (U * (1.1 * (d // H + 4) + 1) * big_s + U * (n + 24) * big_a).reshape(-1)
+        assert np.all(np.abs((got[0] - av[at + i]).double().cpu().numpy()) <= tol + 1e-30)
+    h.close()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "fp32"])
+@pytest.mark.parametrize("div,nb", [(0.301, 128), (0.2, 100)])
+def test_gaps_of_every_size(fmt, div, nb):
+    """Rows older than the cached ones (gap 0), gaps around 2^31 s and near 2^62, with the bins
+    (divisor above 0.223) and with the search."""
+    d, H, ps, n = 128, 2, 16, 75
+    h = _handle(d, H, fmt, nb=nb, div=div)
+    pool = _Pool(d, H, fmt, ps, [n] * 4, seed=43)
+    t = np.concatenate([[0] * 5, [1, 2, 3, 4, 5, 6, 7, 8], 2 ** 31 + np.arange(-6, 7),
+                        2 ** 32 + np.arange(-3, 4), 2 ** 40 + np.arange(7), [2 ** 61] * 5,
+                        2 ** 62 - 1 - np.arange(30, 0, -1)]).astype(np.int64)
+    assert len(t) == n
+    _write(h, pool, _rows(4 * n, d, fmt, 44), [n] * 4, [0] * 4, torch.from_numpy(np.tile(t, 4)).cuda())
+    uvqk, _ = _query(d, fmt, [1] * 4, seed=45)
+    ts = torch.tensor([0, 2 ** 32 + 4, 2 ** 31 - 2, 2 ** 62 - 1], device="cuda")
+    rp, rt = _tables(128, nb, seed=46)
+    av = _attend(h, pool, uvqk, [1] * 4, [n] * 4, ts, rp, rt)
+    torch.cuda.synchronize()
+    assert h.device_error() == 0
+    _check(av, pool, uvqk, [1] * 4, [n] * 4, ts, rp, rt,
+           oracle_cfg(d, H, n_norm=N_NORM, time_buckets=nb, div=div))
+    h.close()
+
+
+@pytest.mark.parametrize("fmt,d,H,ps,pages", [("bf16", 256, 4, 256, 17000),
+                                              ("e4m3", 512, 8, 256, 17000)])
+def test_pages_behind_the_first_four_gigabytes(fmt, d, H, ps, pages):
+    """Byte offsets above 2^32: pages at both ends of a large pool."""
+    lens = [300, 513]
+    h = _handle(d, H, fmt, rows=1024)
+    pool = _Pool(d, H, fmt, ps, lens, seed=47)
+    shape = (pages, H, 2, ps, d // H)
+    pool.num = pages
+    pool.kv = torch.zeros(shape, dtype=pool.kv.dtype, device="cuda")
+    assert pool.kv.numel() * pool.kv.element_size() > 2 ** 32
+    pool.scales = torch.zeros(shape[:-1], dtype=torch.uint8, device="cuda") if fmt == "e4m3" else None
+    pool.ts = torch.zeros((pages, ps), dtype=torch.int64, device="cuda")
+    pool.table = _i32([pages - 1, 0, 0, pages - 3, 1, pages - 2]).view(2, 3)
+    x = _rows(sum(lens), d, fmt, 48)
+    t = torch.arange(sum(lens), device="cuda") * 700
+    _write(h, pool, x, lens, [0, 0], t)
+    out, t_out = torch.zeros_like(x), torch.zeros_like(t)
+    hstu.hstu_pages_read(h.h, pool.struct, pool.table, 3, None, _offsets(lens), 2, sum(lens), out,
+                         t_out, torch.cuda.current_stream())
+    uvqk, ts = _query(d, fmt, [1, 1], seed=49)
+    rp, rt = _tables(128, 128, seed=50)
+    av = _attend(h, pool, uvqk, [1, 1], lens, ts, rp, rt)
+    # the same rows in a small pool
+    small = _Pool(d, H, fmt, ps, lens, seed=47)
+    _write(h, small, x, lens, [0, 0], t)
+    ref = _attend(h, small, uvqk, [1, 1], lens, ts, rp, rt)
+    torch.cuda.synchronize()
+    assert h.device_error() == 0
+    assert torch.equal(av, ref) and torch.equal(t_out, t)
+    w = x.double().cpu().numpy().reshape(-1, 4, H, d // H)
+    want = ph.quantised(w) if fmt == "e4m3" else w
+    got = out.double().cpu().numpy().reshape(-1, 4, H, d // H)
+    assert np.array_equal(got[:, [1, 3]], want[:, [1, 3]])
+    h.close()
+
+
+def test_shared_pages_and_two_graphs_of_one_handle():
+    """Two users over the same pages read alike; graphs of one handle replayed in turn on one
+    stream share its workspace and give what the calls give."""
+    d, H, ps = 512, 8, 64
+    h = _handle(d, H, "e4m3", rows=16384)
+    pool = _filled(h, d, H, "e4m3", ps, [9000, 100], seed=51)
+    table = pool.table.clone()
+    pool.table = torch.stack([table[0], table[0], table[1]]).contiguous()
+    lens, counts = [9000, 9000, 70], [1, 1, 1]
+    uvqk, ts = _query(d, "e4m3", counts, seed=52)
+    uvqk[1], ts[1] = uvqk[0], ts[0]
+    rp, rt = _tables(128, 128, seed=53)
+    a = _attend(h, pool, uvqk, counts, lens, ts, rp, rt)
+    assert torch.equal(a[0], a[1])
+    cases = []
+    for k, (c, l) in enumerate([([1, 1, 1], lens), ([0, 1, 0], [0, 8111, 0])]):
+        r = sum(c)
+        u, t = uvqk[:r].contiguous(), ts[:r].contiguous()
+        off, length, av = _offsets(c), _i32(l), torch.zeros((r, d), device="cuda")
+        call = lambda u=u, t=t, off=off, length=length, av=av, r=r: hstu.hstu_pages_attention(
+            h.h, pool.struct, u, r, off, 3, t, pool.table, pool.width, length, rp, rt, av,
+            torch.cuda.current_stream())
+        call()
+        torch.cuda.synchronize()
+        ref = av.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        cases.append((g, av, ref, (off, length, u, t)))
+    for _ in range(3):
+        for g, av, ref, _ in cases:
+            av.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for _, av, ref, _ in cases:
+            assert torch.equal(av, ref)
+    assert h.device_error() == 0
+    h.close()
