@@ -184,8 +184,9 @@ struct Chunks {
 // by its instructions.  All of a lane's loads (d 1024: 8) are on their way
 // before the row's place is looked up; the scale bytes of a block's eight rows
 // are gathered and stored as one where they are neighbours, since a store of one
-// byte costs as much as one of 32 (65536 rows of d 1024 to e4m3 pages: 80 us with
-// 20 instructions a value more and a store a byte, 149 with one load at a time).
+// byte costs as much as one of 32.  65536 rows of d 1024 to e4m3 pages: 74 us, 5.5
+// TB/s (149 with one load at a time and 25 instructions a value, 12 now; 78 with
+// a store a scale byte; 65.6 with nothing to compute).
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const PagesArgs a) {
   using C = Chunks<FMT, HD>;

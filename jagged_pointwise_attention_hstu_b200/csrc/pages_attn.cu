@@ -36,6 +36,13 @@
 //    bf16 pieces (8 + 8 + 8 bits) or two fp16 ones (11 + 11).
 // fp32 pages (the fp32 path, small models) take the same units with loads
 // straight into registers and fp32 arithmetic.
+//
+// Measured (B200, warm calls): 8 users of 8192 rows, d 1024, bf16 52 us (5.2 TB/s;
+// 48.6 with the arithmetic left out); 256 of 4096, d 512, e4m3 198 to 209 us (5.3
+// to 5.6 TB/s; 175); 168 of 2080, d 768, bf16 170 us (6.3 TB/s); 1 of 100003, d
+// 512, e4m3 28.7 us (3.7 TB/s; 25.1: the start takes 4 us, the join 3).  What bounds
+// e4m3 at head dim 64 besides memory are the instructions of the three blocks an SM
+// holds (64 conversions a step of 32 keys).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -94,6 +101,7 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+
 // What a variant of the kernel is made of.  NT: tiles of 8 columns of P (fp32 pages: rows).
 // Row 4i + t of q has its pieces in columns that lane t of a quad holds: 0 and 1 in tile i at
 // 2t and 2t + 1; a third one in tile 2 at 2t + i, or, with one tile for two rows, at
