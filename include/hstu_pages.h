@@ -59,7 +59,15 @@ typedef struct {
  * two users share may be read by both; positions that one call writes must be
  * distinct.  Device-side findings set HSTU_DEVERR_OFFSETS, _PAGES or
  * _TIMESTAMPS in the handle's error word; the user or row they concern is
- * skipped and its outputs are undefined. */
+ * skipped and its outputs are undefined (offsets that fall or leave the rows
+ * concern every user: the attention then writes nothing).
+ *
+ * The attention uses the handle's workspace: the calls of one handle, and the
+ * replays of its captured calls, must not overlap.  Its waits are bounded as
+ * hstu_set_wait_limit says; one that expires sets HSTU_DEVERR_TIMEOUT, and the
+ * handle's attention over pages is undefined until hstu_get_device_error has been
+ * called.  Infinities and NaN among the q, k and v of a row or the keys and values it
+ * sees make its outputs of that head non-finite or NaN, not more. */
 
 /* Writes (and quantises) rows into pages: row offsets[b] + i of `uvqk` becomes
  * position start[b] + i of user b.

@@ -194,6 +194,9 @@ struct Team {
     if (kAll == 32) __syncwarp();
     else __syncthreads();
   }
+  static __device__ __forceinline__ bool any(bool x) {
+    return kAll == 32 ? __any_sync(0xffffffffu, x) : __syncthreads_or(x) != 0;
+  }
   // Sum of each thread's x, and that of the threads before; `sums` may be used again behind a sync.
   static __device__ __forceinline__ int32_t scan(int32_t x, int32_t* sums, int32_t& before) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -235,7 +238,8 @@ __device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl) {
   }
   const int32_t total = T::scan(mine, pl.sums, before);
   if (blockIdx.x == 0 && err != 0) atomicOr(a.error, err);   // by every team alike
-  if (total == 0) return false;
+  // users whose rows overlap could have more units than 32 bits count
+  if (T::any((err & HSTU_DEVERR_OFFSETS) != 0) || total == 0) return false;
   const int32_t share = (total + gridDim.x - 1) / gridDim.x;
   T::sync();
   int32_t items = 0, items_before;
@@ -262,7 +266,7 @@ __device__ __forceinline__ bool make_plan(const PagesArgs& a, Plan& pl) {
     int32_t at = runs ? before : items_before;
     if (u < at || u >= at + (runs ? mine : items)) continue;
 #pragma unroll 1
-    for (int32_t b = b0;; ++b) {
+    for (int32_t b = b0; b < b1; ++b) {
       int e = 0;
       const User x = user_of<S>(a, b, e);
       const int32_t pieces = runs ? x.nu : (x.nu + share - 1) / share;

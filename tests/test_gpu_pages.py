@@ -623,3 +623,25 @@ def test_shared_pages_and_two_graphs_of_one_handle():
             assert torch.equal(av, ref)
     assert h.device_error() == 0
     h.close()
+
+
+@pytest.mark.parametrize("users", [64, 130])
+@pytest.mark.parametrize("fmt,d,H", [("bf16", 512, 4), ("e4m3", 256, 4), ("fp32", 256, 4)])
+def test_rows_that_overlap_are_reported_whatever_they_add_up_to(fmt, d, H, users):
+    """Offsets 0, R, 0, R, ...: half the users have all rows, and with histories of four
+    million rows 2^33 units of work and more, which no 32-bit count holds."""
+    R, ps, width = 4096, 256, 16380
+    h = _handle(d, H, fmt, rows=R, users=users)
+    pool = _Pool(d, H, fmt, ps, [ps])
+    table = torch.full((users, width), int(pool.table[0, 0]), dtype=torch.int32, device="cuda")
+    offs = _i32([0 if b % 2 == 0 else R for b in range(users + 1)])
+    lens = _i32([width * ps] * users)
+    uvqk = _rows(R, d, fmt, seed=50)
+    ts = torch.zeros(R, dtype=torch.int64, device="cuda")
+    rab = torch.zeros(129, device="cuda")
+    av = torch.full((R, d), 7.0, device="cuda")
+    hstu.hstu_pages_attention(h.h, pool.struct, uvqk, R, offs, users, ts, table, width, lens,
+                              rab, rab, av, torch.cuda.current_stream())
+    assert h.device_error() == hstu.HSTU_DEVERR_OFFSETS
+    assert torch.all(av == 7.0)
+    h.close()
