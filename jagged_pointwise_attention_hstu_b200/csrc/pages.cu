@@ -194,6 +194,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const Pages
   static_assert(kRowWarps == 8, "scales of a block's rows are eight bytes");
   __shared__ __align__(8) uint8_t s_scale[kScaled ? 32 : 1][kRowWarps];   // at most 16 heads
   __shared__ int32_t s_row[kRowWarps];
+  let_next_kernel_start();
+  wait_for_earlier_kernels();
   check_offsets(a);
   const int warp = threadIdx.x >> 5;
   const int32_t r = int32_t(blockIdx.x) * kRowWarps + warp;   // fewer than 2^30
@@ -277,6 +279,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const Pages
 template <int FMT, int HD>
 __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesArgs a) {
   using C = Chunks<FMT, HD>;
+  let_next_kernel_start();
+  wait_for_earlier_kernels();
   check_offsets(a);
   const int32_t r = int32_t(blockIdx.x) * kRowWarps + int32_t(threadIdx.x >> 5);   // fewer than 2^30
   if (r >= a.R) return;
@@ -340,8 +344,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesA
 }  // namespace
 
 #define HSTU_PAGES_ROWS(KERNEL, F, D) \
-  KERNEL<F, D><<<blocks, kRowWarps * 32, 0, st>>>(a); \
-  return cudaGetLastError()
+  return launch_early(KERNEL<F, D>, blocks, kRowWarps * 32, 0, st, a)
 #define HSTU_PAGES_DISPATCH(KERNEL)                                                 \
   if (a.R <= 0 || a.B <= 0) return cudaSuccess;                                     \
   const unsigned blocks = unsigned((a.R + kRowWarps - 1) / kRowWarps);              \

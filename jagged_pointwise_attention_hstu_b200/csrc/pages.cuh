@@ -8,6 +8,34 @@
 
 namespace hstu {
 
+// The kernels of the paged history are launched while the kernel before them in the stream
+// ends, and wait here, every thread and before any access to global memory, until that
+// kernel and all it wrote are complete: the launch and the set-up of the blocks no longer lie
+// between two calls (16 users of up to 4096 rows, d 512, e4m3 12.3 us a call without
+// it and 10.4 with; 1 of 100003 28.7 and 26.6; 8 of 8192, d 1024, bf16 51.5 and 50.0).
+__device__ __forceinline__ void wait_for_earlier_kernels() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the next such kernel take the places of blocks that end.
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, int threads, int smem,
+                         cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = size_t(smem);
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 constexpr int kMinExponent = -126, kMaxExponent = 120;
 
 // The smallest e with m <= 448 * 2^e (448 = 1.75 * 2^8), held in

@@ -494,6 +494,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   __shared__ int32_t s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k4 = lane >> 3, t8 = lane & 7;
+  let_next_kernel_start();
+  wait_for_earlier_kernels();
   fill_time(a, s_time, tid);
   const bool alone = a.B <= kWarpUsers;      // a warp plans for itself
   Plan& plan = plans[alone ? warp : 0];
@@ -692,7 +694,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
     mbar_init(&ring.turn, kWarps);
     fence_mbarrier_init();
   }
+  let_next_kernel_start();
   __syncthreads();
+  wait_for_earlier_kernels();
   // what there is to do is the producer's to know; with many users all threads plan
   const bool alone = a.B <= kWarpUsers;
   if (!alone && !make_plan<S, S::kThreads>(a, plan)) return;
@@ -1201,7 +1205,7 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
   static_assert(S::kHalves * 128 >= S::kRow || !S::kSwizzle, "boxes");
   static_assert(S::kF32 || S::kRingBytes(S::kStages) <= 128 * 1024, "ring");
   if constexpr (S::kF32) {
-    pages_attention_f32_kernel<HD, NT><<<grid_of<S>(a), S::kThreads, 0, st>>>(a);
+    return launch_early(pages_attention_f32_kernel<HD, NT>, grid_of<S>(a), S::kThreads, 0, st, a);
   } else {
     static std::atomic<uint64_t> done{0};
     constexpr int bytes = S::kRingBytes(S::kStages);
@@ -1217,9 +1221,9 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
           !make_tmap_2d_u8_sw128(&block, a.kv, S::kRow, rows, 16))
         return cudaErrorInvalidValue;
     }
-    pages_attention_kernel<FMT, HD, NT><<<grid_of<S>(a), S::kThreads, bytes, st>>>(a, run, block);
+    return launch_early(pages_attention_kernel<FMT, HD, NT>, grid_of<S>(a), S::kThreads, bytes, st,
+                        a, run, block);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

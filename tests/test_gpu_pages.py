@@ -645,3 +645,75 @@ def test_rows_that_overlap_are_reported_whatever_they_add_up_to(fmt, d, H, users
     assert h.device_error() == hstu.HSTU_DEVERR_OFFSETS
     assert torch.all(av == 7.0)
     h.close()
+
+
+@pytest.mark.parametrize("fmt,d,H,ps", [("fp32", 64, 2, 16), ("bf16", 256, 4, 16),
+                                        ("e4m3", 512, 4, 64)])
+@pytest.mark.parametrize("how", ["eager", "captured"])
+def test_calls_that_follow_each_other_see_what_the_last_one_wrote(fmt, d, H, ps, how):
+    """Attention, write and read of growing histories with nothing between the launches: the
+    bits of the same calls with a wait after each.  The capture begins behind a copy and a
+    fill, and holds a call that joins two branches."""
+    lens, steps = [30, 0, 200, 47], 12
+    h = _handle(d, H, fmt)
+    B = len(lens)
+    room = _filled(h, d, H, fmt, ps, [n + steps for n in lens], seed=60)
+    rp, rt = _tables(128, 128, seed=61)
+    off = _offsets([1] * B)
+    rows = [_query(d, fmt, [1] * B, seed=62 + i) for i in range(steps)]
+    at = [_i32([n + i for n in lens]) for i in range(steps)]
+    first = [room.kv.clone(), room.ts.clone()] + ([room.scales.clone()] if fmt == "e4m3" else [])
+    held = [x for x in (room.kv, room.ts, room.scales) if x is not None]
+    av = torch.zeros((steps, B, d), device="cuda")
+    back = torch.zeros((steps, B, 4 * d), dtype=rows[0][0].dtype, device="cuda")
+
+    def step(i, st, wait):
+        uvqk, ts = rows[i]
+        hstu.hstu_pages_attention(h.h, room.struct, uvqk, B, off, B, ts, room.table, room.width,
+                                  at[i], rp, rt, av[i], st)
+        wait()
+        hstu.hstu_pages_write(h.h, room.struct, uvqk, B, off, B, ts, room.table, room.width,
+                              at[i], st)
+        wait()
+        hstu.hstu_pages_read(h.h, room.struct, room.table, room.width, at[i], off, B, B, back[i],
+                             None, st)
+        wait()
+
+    for i in range(steps):
+        step(i, torch.cuda.current_stream(), torch.cuda.synchronize)
+    want_av, want_back = av.clone(), back.clone()
+    want = [x.clone() for x in held]
+    assert torch.equal(back[:, :, d:2 * d], torch.stack([r[0] for r in rows])[:, :, d:2 * d]) \
+        or fmt == "e4m3"
+    side, branch = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            if how == "eager":
+                for x, y in zip(held, first):
+                    x.copy_(y)
+                av.zero_()
+                for i in range(steps):
+                    step(i, side, lambda: None)
+            else:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=side):
+                    for x, y in zip(held, first):
+                        x.copy_(y)
+                    av.zero_()
+                    for i in range(steps):
+                        if i == 5:
+                            branch.wait_stream(side)
+                            with torch.cuda.stream(branch):
+                                back[i].zero_()
+                            side.wait_stream(branch)
+                        step(i, side, lambda: None)
+                graph.replay()
+                graph.replay()
+        torch.cuda.synchronize()
+        assert h.device_error() == 0
+        assert torch.equal(av, want_av) and torch.equal(back, want_back)
+        bits = torch.int32 if fmt == "fp32" else torch.int16 if fmt == "bf16" else torch.uint8
+        assert torch.equal(held[0].view(bits), want[0].view(bits))
+        assert all(torch.equal(x, y) for x, y in zip(held[1:], want[1:]))
+    h.close()
