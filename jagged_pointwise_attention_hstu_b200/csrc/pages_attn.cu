@@ -37,12 +37,12 @@
 // fp32 pages (the fp32 path, small models) take the same units with loads
 // straight into registers and fp32 arithmetic.
 //
-// Measured (B200, warm calls): 8 users of 8192 rows, d 1024, bf16 52 us (5.2 TB/s;
-// 48.6 with the arithmetic left out); 256 of 4096, d 512, e4m3 198 to 209 us (5.3
-// to 5.6 TB/s; 175); 168 of 2080, d 768, bf16 170 us (6.3 TB/s); 1 of 100003, d
-// 512, e4m3 28.7 us (3.7 TB/s; 25.1: the start takes 4 us, the join 3).  What bounds
-// e4m3 at head dim 64 besides memory are the instructions of the three blocks an SM
-// holds (64 conversions a step of 32 keys).
+// Measured (B200, warm calls, a call's share of a graph of 21): 8 users of 8192 rows, d 1024,
+// bf16 49.5 us (5.4 TB/s); 256 of 4096, d 512, e4m3 187 to 201 us (5.5 to 5.9 TB/s; 175
+// with the arithmetic left out); 168 of 2080, d 768, bf16 167 us (6.4 TB/s); 1 of 100003,
+// d 512, e4m3 26.1 us (4.0 TB/s: the start takes 4 us, the join 3); 1 of 37, d 256 5.4 us.
+// What bounds e4m3 at head dim 64 besides memory is the latency of the 12 warps an SM holds
+// (a step of 32 keys is 230 instructions, 66 of them conversions).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
