@@ -179,15 +179,19 @@ def _check(status: int, what: str) -> None:
 def _ptr(t) -> Optional[int]:
     try:
         return t.data_ptr()
-    except AttributeError:   # an address, or None
-        return t
+    except AttributeError:
+        if t is None or isinstance(t, int):   # an address
+            return t
+        raise                # ctypes would take whatever has an _as_parameter_, a stream too
 
 
 def _stream_ptr(stream) -> Optional[int]:
     try:
         return stream.cuda_stream
-    except AttributeError:   # a cudaStream_t, or None
-        return stream
+    except AttributeError:
+        if stream is None or isinstance(stream, int):   # a cudaStream_t
+            return stream
+        raise
 
 
 # ----------------------------------------------------------------- entry points

@@ -7,6 +7,7 @@ import subprocess
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 from oracle import paged_history as ph
@@ -137,3 +138,21 @@ int main(void) {
                     "-lhstu", "-Wl,-rpath," + libdir], check=True)
     out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout
     assert out.split() == [str(hstu.HSTU_ERR_INVALID_ARG)] * 5
+
+
+def test_bindings_take_tensors_and_addresses_and_nothing_else():
+    """An object that ctypes would accept as a pointer by itself (a stream has an
+    _as_parameter_) must not become a tensor's address, nor a tensor a stream."""
+    class Handle:
+        _as_parameter_ = ctypes.c_void_p(64)
+
+    x = torch.zeros(4)
+    assert hstu._ptr(x) == x.data_ptr() and hstu._ptr(None) is None and hstu._ptr(64) == 64
+    assert hstu._stream_ptr(None) is None and hstu._stream_ptr(64) == 64
+    for bad in (Handle(), ctypes.c_void_p(64), "x", [1]):
+        with pytest.raises(AttributeError):
+            hstu._ptr(bad)
+        with pytest.raises(AttributeError):
+            hstu._stream_ptr(bad)
+    with pytest.raises(AttributeError):
+        hstu._stream_ptr(x)
