@@ -717,3 +717,47 @@ def test_calls_that_follow_each_other_see_what_the_last_one_wrote(fmt, d, H, ps,
         assert torch.equal(held[0].view(bits), want[0].view(bits))
         assert all(torch.equal(x, y) for x, y in zip(held[1:], want[1:]))
     h.close()
+
+
+def test_two_handles_on_two_streams_over_one_pool():
+    """Calls of two handles that overlap in time, one of them with kernel timing on: the bits
+    of the same calls one after the other."""
+    d, H, ps, lens = 512, 8, 64, [900, 64, 3000, 0, 700]
+    hs = [_handle(d, H, "e4m3", rows=8192) for _ in range(2)]
+    pool = _filled(hs[0], d, H, "e4m3", ps, lens, seed=70)
+    rp, rt = _tables(128, 128, seed=71)
+    counts = [[1, 1, 1, 1, 1], [4, 0, 9, 2, 1]]
+    qs = [_query(d, "e4m3", c, seed=72 + i) for i, c in enumerate(counts)]
+    off, length = [_offsets(c) for c in counts], _i32(lens)
+    want = [_attend(h, pool, q, c, lens, t, rp, rt) for h, c, (q, t) in zip(hs, counts, qs)]
+    hstu.hstu_set_kernel_timing(hs[1].h, True)
+    avs = [torch.zeros((40,) + tuple(w.shape), device="cuda") for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in hs]
+    for i in range(40):
+        for h, c, (q, t), o, av, st in zip(hs, counts, qs, off, avs, streams):
+            hstu.hstu_pages_attention(h.h, pool.struct, q, sum(c), o, len(c), t, pool.table,
+                                      pool.width, length, rp, rt, av[i], st)
+    torch.cuda.synchronize()
+    for h, w, av in zip(hs, want, avs):
+        assert h.device_error() == 0
+        assert torch.equal(av, w[None].expand_as(av))
+        h.close()
+
+
+def test_calls_on_the_default_stream():
+    d, H, ps, lens = 256, 4, 16, [70, 5, 0]
+    h = _handle(d, H, "bf16")
+    pool = _filled(h, d, H, "bf16", ps, lens, seed=80)
+    uvqk, ts = _query(d, "bf16", [1, 1, 1], seed=81)
+    rp, rt = _tables(128, 128, seed=82)
+    torch.cuda.synchronize()
+    want = _attend(h, pool, uvqk, [1, 1, 1], lens, ts, rp, rt, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    off, length, av = _offsets([1, 1, 1]), _i32(lens), torch.zeros((20, 3, d), device="cuda")
+    for i in range(20):
+        hstu.hstu_pages_attention(h.h, pool.struct, uvqk, 3, off, 3, ts, pool.table, pool.width,
+                                  length, rp, rt, av[i], None)
+    torch.cuda.synchronize()
+    assert h.device_error() == 0 and torch.equal(av, want[None].expand_as(av))
+    h.close()
