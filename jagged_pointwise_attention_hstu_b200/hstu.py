@@ -177,19 +177,23 @@ def _check(status: int, what: str) -> None:
 
 
 def _ptr(t) -> Optional[int]:
+    if t is None:
+        return None
     try:
         return t.data_ptr()
     except AttributeError:
-        if t is None or isinstance(t, int):   # an address
+        if isinstance(t, int):                # an address
             return t
         raise                # ctypes would take whatever has an _as_parameter_, a stream too
 
 
 def _stream_ptr(stream) -> Optional[int]:
+    if stream is None:
+        return None
     try:
         return stream.cuda_stream
     except AttributeError:
-        if stream is None or isinstance(stream, int):   # a cudaStream_t
+        if isinstance(stream, int):           # a cudaStream_t
             return stream
         raise
 
