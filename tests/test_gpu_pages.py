@@ -761,3 +761,71 @@ def test_calls_on_the_default_stream():
     torch.cuda.synchronize()
     assert h.device_error() == 0 and torch.equal(av, want[None].expand_as(av))
     h.close()
+
+
+@pytest.mark.parametrize("fmt,d,H,ps", [
+    ("fp32", 64, 2, 16), ("fp32", 128, 1, 64), ("fp32", 256, 8, 32), ("bf16", 128, 2, 16),
+    ("bf16", 384, 3, 32), ("bf16", 512, 8, 64), ("e4m3", 128, 1, 64), ("e4m3", 256, 4, 16),
+    ("e4m3", 384, 6, 256), ("e4m3", 512, 4, 32), ("e4m3", 768, 12, 16)])
+def test_large_writes_and_reads_are_those_of_their_parts(fmt, d, H, ps):
+    """A call of many rows (several a warp) writes and reads, bit for bit, what calls of a few
+    hundred of the same rows do (which are the oracle's, above); ragged users, empty ones
+    among them, any first position, rows behind the last sequence, errors left aside."""
+    users, R = 300, 13001
+    rng = np.random.default_rng(d)
+    counts = rng.multinomial(R - 40, rng.dirichlet(np.full(users, 0.4)))
+    counts[rng.integers(0, users, 60)] = 0
+    counts[7] += 1
+    start = rng.integers(0, 2 * ps, users)
+    n = int(counts.sum())
+    h = _handle(d, H, fmt, rows=R, users=users)
+    uvqk = _rows(R, d, fmt, seed=d + 1, scale=8.0)
+    ts = torch.arange(R, dtype=torch.int64, device="cuda") * 7 + 1
+    pools = [_Pool(d, H, fmt, ps, [int(c + s) for c, s in zip(counts, start)], seed=d)
+             for _ in range(2)]
+    off = np.concatenate([[0], np.cumsum(counts)])
+    _write_rows = lambda p, x, t, o, b0, b1: hstu.hstu_pages_write(
+        h.h, p.struct, x, x.shape[0], _i32(o), b1 - b0, t, p.table[b0:], p.width,
+        _i32(start[b0:b1]), torch.cuda.current_stream())
+    _write_rows(pools[0], uvqk, ts, off, 0, users)
+    groups = [(b, min(b + 20, users)) for b in range(0, users, 20)]
+    for b0, b1 in groups:
+        lo, hi = int(off[b0]), int(off[b1])
+        if hi > lo:
+            # a copy: pointers are 16-byte aligned
+            _write_rows(pools[1], uvqk[lo:hi].clone(), ts[lo:hi].clone(), off[b0:b1 + 1] - lo, b0, b1)
+    bits = torch.int32 if fmt == "fp32" else torch.int16 if fmt == "bf16" else torch.uint8
+    assert torch.equal(pools[0].table, pools[1].table)
+    assert torch.equal(pools[0].kv.view(bits), pools[1].kv.view(bits))
+    assert torch.equal(pools[0].ts, pools[1].ts)
+    assert fmt != "e4m3" or torch.equal(pools[0].scales, pools[1].scales)
+    out = torch.full_like(uvqk, 7.0)
+    ts_out = torch.full_like(ts, -7)
+    hstu.hstu_pages_read(h.h, pools[0].struct, pools[0].table, pools[0].width, _i32(start),
+                         _i32(off), users, R, out, ts_out, torch.cuda.current_stream())
+    assert torch.all(out[n:] == 7.0) and torch.all(ts_out[n:] == -7)
+    assert torch.equal(ts_out[:n], ts[:n])
+    assert torch.all(out[:, :d] == 7.0) and torch.all(out[:, 2 * d:3 * d] == 7.0)
+    for b0, b1 in groups:
+        lo, hi = int(off[b0]), int(off[b1])
+        if hi > lo:
+            part = torch.full((hi - lo, 4 * d), 7.0, dtype=uvqk.dtype, device="cuda")
+            hstu.hstu_pages_read(h.h, pools[0].struct, pools[0].table[b0:].clone(), pools[0].width,
+                                 _i32(start[b0:b1]), _i32(off[b0:b1 + 1] - lo), b1 - b0, hi - lo,
+                                 part, None, torch.cuda.current_stream())
+            assert torch.equal(out[lo:hi], part)
+    if fmt != "e4m3":
+        assert torch.equal(out[:n, d:2 * d], uvqk[:n, d:2 * d])
+        assert torch.equal(out[:n, 3 * d:], uvqk[:n, 3 * d:])
+    # a bad page of one user: the others' rows all the same
+    b = int(np.argmax(counts))
+    pools[0].table[b] = -1
+    again = torch.full_like(uvqk, 7.0)
+    assert h.device_error() == 0
+    hstu.hstu_pages_read(h.h, pools[0].struct, pools[0].table, pools[0].width, _i32(start),
+                         _i32(off), users, R, again, None, torch.cuda.current_stream())
+    assert h.device_error() == hstu.HSTU_DEVERR_PAGES
+    lo, hi = int(off[b]), int(off[b + 1])
+    assert torch.all(again[lo:hi] == 7.0)
+    assert torch.equal(again[:lo], out[:lo]) and torch.equal(again[hi:], out[hi:])
+    h.close()
