@@ -32,13 +32,12 @@ constexpr int kRowWarps = 8;   // warps per block of the write and read kernels
 
 // The largest b with offs[b] <= r, for 0 <= r < offs[B], found by the whole
 // warp: 32 probes a step, so one step for up to 32 users and two for 1024.
-__device__ __forceinline__ int32_t user_of_row(const int32_t* __restrict__ offs, int32_t B,
-                                               int64_t r, int lane) {
+__device__ __forceinline__ int32_t user_of_row(const int32_t* offs, int32_t B, int64_t r, int lane) {
   int32_t lo = 0, n = B;   // the answer is in [lo, lo + n)
   while (n > 1) {
     const int32_t step = (n + 31) >> 5;
     const int32_t k = lane * step;
-    const bool le = k < n && __ldg(offs + lo + k) <= r;
+    const bool le = k < n && fetch(offs + lo + k) <= r;
     const unsigned m = __ballot_sync(0xffffffffu, le);
     const int32_t top = m == 0 ? 0 : 31 - __clz(m);
     lo += top * step;
@@ -60,20 +59,19 @@ __device__ __forceinline__ void check_offsets(const PagesArgs& a) {
   if (blockIdx.x != 0) return;
   bool bad = false;
   for (int32_t i = threadIdx.x; i < a.B; i += blockDim.x) {
-    const int32_t lo = __ldg(a.offsets + i), hi = __ldg(a.offsets + i + 1);
+    const int32_t lo = fetch(a.offsets + i), hi = fetch(a.offsets + i + 1);
     bad |= lo > hi || (i == 0 && lo != 0) || (i == a.B - 1 && hi > a.R);
   }
   if (bad) atomicOr(a.error, HSTU_DEVERR_OFFSETS);
 }
 
 // The same for a lane's own row, r >= the row that user b has.
-__device__ __forceinline__ int32_t user_from(const int32_t* __restrict__ offs, int32_t B, int32_t r,
-                                             int32_t b) {
-  if (b + 1 >= B || __ldg(offs + b + 1) > r) return b;
+__device__ __forceinline__ int32_t user_from(const int32_t* offs, int32_t B, int32_t r, int32_t b) {
+  if (b + 1 >= B || fetch(offs + b + 1) > r) return b;
   int32_t lo = b + 1, hi = B;
   while (hi - lo > 1) {
     const int32_t mid = (lo + hi) >> 1;
-    if (__ldg(offs + mid) <= r) lo = mid; else hi = mid;
+    if (fetch(offs + mid) <= r) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -93,16 +91,16 @@ __device__ __forceinline__ Place place_of(const PagesArgs& a, int32_t r, int lan
     if (lane >= ROWS || r >= a.R) return p;
     b = user_from(a.offsets, a.B, r, b);
   }
-  const int32_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
+  const int32_t r0 = fetch(a.offsets + b), r1 = fetch(a.offsets + b + 1);
   // behind the last sequence, or a table that check_offsets reports
   if (r < r0 || r >= r1 || r0 < 0 || r1 > a.R) return p;
   p.err = HSTU_DEVERR_PAGES;
   if (a.one_row && r1 - r0 > 1) return p;
-  const int32_t first = a.lengths != nullptr ? __ldg(a.lengths + b) : 0;
+  const int32_t first = a.lengths != nullptr ? fetch(a.lengths + b) : 0;
   if (first < 0 || first >= (1 << 30)) return p;       // positions end at 2^30, rows too
   const int32_t pos = first + (r - r0), k = pos >> a.page_shift;
   if (k >= int32_t(a.width)) return p;
-  const int32_t page = __ldg(a.table + (int64_t(b) * int32_t(a.width) + k));
+  const int32_t page = fetch(a.table + (int64_t(b) * int32_t(a.width) + k));
   if (page < 0 || page >= a.num_pages) return p;
   const int32_t slot = pos & ((1 << a.page_shift) - 1);
   p.row = ((page * a.H * 2) << a.page_shift) + slot;
@@ -232,8 +230,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_write_kernel(const Pages
       for (int i = 0; i < kBatch; ++i) {
         const int c = c0 + 32 * i + lane;
         const bool on = r + j < a.R && c < ch.each;
-        v[0][j][i] = on ? __ldg(keys + c) : make_uint4(0u, 0u, 0u, 0u);
-        v[1][j][i] = on ? __ldg(vals + c) : make_uint4(0u, 0u, 0u, 0u);
+        v[0][j][i] = on ? fetch(keys + c) : make_uint4(0u, 0u, 0u, 0u);
+        v[1][j][i] = on ? fetch(vals + c) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
   };
@@ -339,12 +337,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesA
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if constexpr (FMT != HSTU_PAGES_E4M3) {
-            v[x][j][i] = __ldg(from + at + x * plane * C::kPerHead);
+            v[x][j][i] = fetch(from + at + x * plane * C::kPerHead);
           } else {
-            const uint2 q = __ldg(codes + at + x * plane * C::kPerHead);
+            const uint2 q = fetch(codes + at + x * plane * C::kPerHead);
             v[x][j][i].x = q.x;
             v[x][j][i].y = q.y;
-            s[x][j][i] = block_scale(__ldg(scales + block + x * plane));
+            s[x][j][i] = block_scale(fetch(scales + block + x * plane));
           }
         }
       }

@@ -20,6 +20,15 @@ __device__ __forceinline__ void wait_for_earlier_kernels() {
 __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// Behind that wait the caller's memory is read by ordinary loads (and bulk copies), never
+// by __ldg: the read-only path takes what it reads for constant while the kernel runs, may
+// keep lines that an SM read for the kernel before last, and its loads are not ordered behind
+// the wait; the kernel before this one, which may still run when this one starts, writes pages,
+// scales, times and rows.  Only the handle's own tables are constant.
+template <class T>
+__device__ __forceinline__ T fetch(const T* p) {
+  return *p;
+}
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), unsigned blocks, int threads, int smem,
                          cudaStream_t st, const A&... args) {

@@ -154,8 +154,8 @@ struct User {
 template <class S>
 __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err) {
   User u;
-  const int32_t r0 = __ldg(a.offsets + b), r1 = __ldg(a.offsets + b + 1);
-  u.n = __ldg(a.lengths + b);
+  const int32_t r0 = fetch(a.offsets + b), r1 = fetch(a.offsets + b + 1);
+  u.n = fetch(a.lengths + b);
   if (r0 < 0 || r1 < r0 || r1 > a.R || (b == 0 && r0 != 0)) err |= HSTU_DEVERR_OFFSETS;
   if (u.n < 0 || u.n > (a.width << a.page_shift)) err |= HSTU_DEVERR_PAGES;
   u.r0 = r0;
@@ -370,13 +370,13 @@ __device__ __forceinline__ void fill_time(const PagesArgs& a, int4* s_time, int 
   const int cand = __ldg(a.time_lut + k);
   const int next = cand + 1 < a.time_buckets ? cand + 1 : a.time_buckets - 1;
   s_time[k] = make_int4(cand + 1 < a.time_buckets ? __ldg(a.thr32 + cand + 1) : 0x7FFFFFFF,
-                        __float_as_int(__ldg(a.rab_time + cand)),
-                        __float_as_int(__ldg(a.rab_time + next)), 0);
+                        __float_as_int(fetch(a.rab_time + cand)),
+                        __float_as_int(fetch(a.rab_time + next)), 0);
 }
 
 // rab_pos for key j of the n cached, with pos_far what most have.
 __device__ __forceinline__ float pos_bias(const PagesArgs& a, float pos_far, int32_t n, int32_t j) {
-  return n - j < a.pos_clamp ? __ldg(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
+  return n - j < a.pos_clamp ? fetch(a.rab_pos + (j < n ? n - j : 0)) : pos_far;
 }
 
 // Whether the bins serve a gap (from 0 to 2^31 - 3 s), and what they say: bin 4e + m of
@@ -390,7 +390,7 @@ __device__ __forceinline__ float bin_bias(const int4* s_time, uint32_t gap) {
 }
 __device__ __forceinline__ float time_bias(const PagesArgs& a, const int4* s_time, int64_t gap) {
   return bin_gap(a, gap) ? bin_bias(s_time, uint32_t(gap))
-                         : __ldg(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
+                         : fetch(a.rab_time + time_bucket(a.thresholds, a.time_buckets, gap));
 }
 __device__ __forceinline__ int64_t gap_of(int64_t now, int64_t then) {
   return int64_t(uint64_t(now) - uint64_t(then));   // any two timestamps: no signed overflow
@@ -502,8 +502,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
   if (!(alone ? make_plan<S, 32>(a, plan) : make_plan<S, S::kThreads>(a, plan))) return;
   __syncthreads();
   Walk<S> walk(a, plan, true);
-  const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
-  const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
+  const float pos_far = fetch(a.rab_pos + a.pos_clamp);
+  const float self_bias = fetch(a.rab_pos) + fetch(a.rab_time);
   const int32_t slot_mask = (1 << a.page_shift) - 1;
   const int64_t plane = int64_t(1) << a.page_shift;
   int err = 0;
@@ -522,11 +522,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int64_t r = p.row0 + (i < p.nq ? i : 0);
-      now[i] = __ldg(a.ts + r);
+      now[i] = fetch(a.ts + r);
       if (now[i] < 0 || now[i] >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.uvqk) +
+        const float4 v = fetch(reinterpret_cast<const float4*>(static_cast<const float*>(a.uvqk) +
                                r * 4 * a.d + 2 * a.d + p.h * HD + 32 * e) + t8);
         q[i][4 * e] = v.x, q[i][4 * e + 1] = v.y, q[i][4 * e + 2] = v.z, q[i][4 * e + 3] = v.w;
         o[i][4 * e] = o[i][4 * e + 1] = o[i][4 * e + 2] = o[i][4 * e + 3] = 0.f;
@@ -537,11 +537,11 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
     for (int32_t tile = p.tile0; tile < p.tile1; ++tile) {
       const int32_t j0 = tile * S::kUnit + warp * S::kStep, jl = j0 + (lane & 15);
       if (j0 < n) {
-        const int32_t page = __ldg(table + (j0 >> a.page_shift));
+        const int32_t page = fetch(table + (j0 >> a.page_shift));
         if (page < 0 || page >= a.num_pages) {
           err |= HSTU_DEVERR_PAGES;
         } else {
-          const int64_t then = __ldg(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
+          const int64_t then = fetch(a.page_ts + (int64_t(page) << a.page_shift) + (jl & slot_mask));
           float bias[NT];                // of the lane's key
 #pragma unroll
           for (int i = 0; i < NT; ++i)
@@ -554,8 +554,8 @@ __global__ void __launch_bounds__(kWarps * 32, (Shape<HSTU_PAGES_FP32, HD, NT>::
 #pragma unroll
             for (int e = 0; e < E; ++e) {
               const float* at = base + int64_t(4 * s + k4) * HD + 32 * e + 4 * t8;
-              k[s][e] = __ldg(reinterpret_cast<const float4*>(at));
-              v[s][e] = __ldg(reinterpret_cast<const float4*>(at + plane * HD));
+              k[s][e] = fetch(reinterpret_cast<const float4*>(at));
+              v[s][e] = fetch(reinterpret_cast<const float4*>(at + plane * HD));
             }
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
@@ -716,10 +716,10 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       auto page_of = [&](int32_t tile) { // of the lane's run; -1: no key there, -2: no such page
         const int64_t j = int64_t(tile) * S::kUnit + (int64_t(lane) << run_shift);
         if (tile >= p.tile1 || (lane << run_shift) >= S::kUnit || j >= p.n) return -1;
-        const int32_t x = __ldg(table + (j >> a.page_shift));
+        const int32_t x = fetch(table + (j >> a.page_shift));
         return x >= 0 && x < a.num_pages ? x : -2;
       };
-      const int64_t now = lane < p.nq ? __ldg(a.ts + p.row0 + lane) : 0;
+      const int64_t now = lane < p.nq ? fetch(a.ts + p.row0 + lane) : 0;
       if (now < 0 || now >= kMaxTimestamp) err |= HSTU_DEVERR_TIMESTAMPS;
       int32_t page_next = page_of(p.tile0);
       for (int32_t tile = p.tile0; tile < p.tile1; ++tile) {
@@ -817,8 +817,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   constexpr int QT = S::kTiles;
   constexpr int kQ = S::kGroup < 4 ? S::kGroup : 4;   // rows of a tile
   const int g = lane >> 2, t = lane & 3;
-  const float pos_far = __ldg(a.rab_pos + a.pos_clamp);
-  const float self_bias = __ldg(a.rab_pos) + __ldg(a.rab_time);
+  const float pos_far = fetch(a.rab_pos + a.pos_clamp);
+  const float self_bias = fetch(a.rab_pos) + fetch(a.rab_time);
   float (*sum)[S::kPad] = s_sum[warp];
   uint16_t (*ps)[S::kStep + 8] = s_p[warp];
   uint32_t turn = 0;
