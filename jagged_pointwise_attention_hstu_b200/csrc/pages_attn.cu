@@ -643,6 +643,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long lo
   return true;
 }
 
+// The same by a whole warp, which gives up as one: lanes look at the clock at different
+// moments, and a lane that left alone would be missing from the warp's next vote.
+__device__ __forceinline__ bool wait_by_all(uint64_t* bar, uint32_t parity, long long limit) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, limit)) != 0;
+}
+
 __device__ __forceinline__ uint2 lds8(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
@@ -726,10 +732,8 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
         const int32_t page = page_next;
         page_next = page_of(tile + 1);
         const int s = issued % S::kStages;
-        if (!wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit)) {
-          ok = false;
-          break;
-        }
+        ok = wait_by_all(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
+        if (!ok) break;
         const int32_t j = tile * S::kUnit + (lane << run_shift);
         // whole blocks of 16 keys: what lies behind the history in the last one is not used
         int32_t keys = page >= 0 ? (p.n - j < run ? (p.n - j + 15) & ~15 : run) : 0;
@@ -795,7 +799,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       }
     }
     const int s = issued % S::kStages;
-    if (ok) ok = wait_for(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
+    if (ok) ok = wait_by_all(&ring.empty[s], ((issued / S::kStages) & 1) ^ 1, limit);
     if (ok && lane == 0) {
       ring.unit[s].what = make_int4(0, 0, kStop, 0);
       mbar_arrive(&ring.full[s]);
@@ -825,9 +829,9 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   auto sync = [&]() {                          // of the warps that compute
     __syncwarp();
     if (lane == 0) mbar_arrive(&ring.turn);
-    const bool ok = wait_for(&ring.turn, turn, limit);
+    const bool ok = wait_by_all(&ring.turn, turn, limit);
     turn ^= 1;
-    return __all_sync(0xffffffffu, ok) != 0;
+    return ok;
   };
   // the 16-byte chunks of a key that are the lane's, and which of its rows a lane's key is
   auto chunk = [&](int y) { return S::kSwizzle ? 2 * t + (y & 1) + 8 * (y >> 1) : t; };
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
   bool fresh = true;                           // the next unit begins a part, or there is none
   uint32_t parity = 0;
   for (int st = 0; up;) {
-    if (__any_sync(0xffffffffu, !wait_for(&ring.full[st], parity, limit))) break;
+    if (!wait_by_all(&ring.full[st], parity, limit)) break;
     const int4 what = ring.unit[st].what;
     if (what.z & kStop) {
       done = true;

@@ -25,3 +25,12 @@ def test_memory_that_another_kernel_may_write_is_read_by_ordinary_loads():
             seen.add(m.group(1))
         assert "__restrict__" not in text and "ld.global.nc" not in text, name
     assert seen <= constant
+
+
+def test_a_warp_gives_up_a_wait_as_one():
+    """Bounded waits are decided by the whole warp: lanes that look at the clock at different
+    moments would part, and the rest wait for them in the next vote."""
+    text = _source("pages_attn.cu")
+    calls = re.findall(r"(?<!bool )\bwait_for\(", text)
+    assert len(calls) == 1 and re.search(r"__all_sync\(0xffffffffu, wait_for\(", text)
+    assert len(re.findall(r"(?<!bool )\bwait_by_all\(", text)) >= 4
