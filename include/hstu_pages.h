@@ -67,7 +67,8 @@ typedef struct {
  * hstu_set_wait_limit says; one that expires sets HSTU_DEVERR_TIMEOUT, and the
  * handle's attention over pages is undefined until hstu_get_device_error has been
  * called.  Infinities and NaN among the q, k and v of a row or the keys and values it
- * sees make its outputs of that head non-finite or NaN, not more. */
+ * sees make its outputs of that head non-finite or NaN, not more; so do finite ones with
+ * a score, or (E4M3) a SiLU(score) * 2^e of a value's block, that fp32 does not hold. */
 
 /* Writes (and quantises) rows into pages: row offsets[b] + i of `uvqk` becomes
  * position start[b] + i of user b.

@@ -951,9 +951,12 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
       if (what.y != 0) mine = mine && !(uint32_t(what.y) >> (kl >> run_shift) & 1);
       const uint8_t* side = stages + S::kStages * S::kDataBytes + st * S::kSideBytes;
       const int64_t then = *reinterpret_cast<const int64_t*>(side + 8 * kl);
-      float ks = 1.f, vs = 1.f;
+      // The key's scale in two factors, one of them 1, with q's between them: a product that fp32
+      // holds is reached without a step beyond it, whichever of the two scales is large.
+      float ks_down = 1.f, ks_up = 1.f, vs = 1.f;
       if constexpr (S::kF16) {
-        ks = block_scale(side[scale_at]);
+        const float ks = block_scale(side[scale_at]);
+        ks_down = fminf(ks, 1.f), ks_up = fmaxf(ks, 1.f);
         vs = block_scale(side[scale_at + run]);
       }
       float s[NB][2][QT];                // of key 16 nb + 8 x + g and row 4i + t
@@ -1007,7 +1010,7 @@ __global__ void __launch_bounds__((Shape<FMT, HD, NT>::kThreads), (Shape<FMT, HD
             const float z = lane & 8 ? y3 : y2;
             y[c] = lane & 16 ? z : y[c];
           }
-          if constexpr (S::kF16) y[c] = y[c] * q_scale[4 * i + c] * ks;
+          if constexpr (S::kF16) y[c] = y[c] * ks_down * q_scale[4 * i + c] * ks_up;
         }
         // lanes without a key take gap 0
         int64_t gap[N];
