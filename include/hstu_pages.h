@@ -97,9 +97,10 @@ hstu_status hstu_pages_read(hstu_handle* h, const hstu_page_pool* pool, const in
  *   s_r = q_r . k_r + rab_pos[0] + rab_time[0]
  *   av[r, h-th head] = (sum_j SiLU(s_j) v_j + SiLU(s_r) v_r) / n_norm
  * with k_r, v_r from the row itself, so the result does not depend on whether
- * the row has been written to a page.  Made for one or a few rows a user; the
- * history is split over the GPU and the parts are joined in a fixed order, so
- * a call gives the same bits every time.
+ * the row has been written to a page.  Made for one or a few rows a user, and
+ * takes more rows of a user at once where R > num_users: leave users without rows
+ * out of a call for several rows of a few.  The history is split over the GPU and
+ * the parts are joined in a fixed order, so a call gives the same bits every time.
  *   uvqk         device [R, 4d] compute dtype (V, Q and K are read)
  *   timestamps   device int64 [R], in [0, 2^62)
  *   lengths      device int32 [num_users]: cached rows of each user, >= 0

@@ -1237,7 +1237,13 @@ cudaError_t launch(const PagesArgs& a, cudaStream_t st) {
 
 cudaError_t launch_pages_attention(const PagesArgs& a, cudaStream_t st) {
   if (a.R <= 0 || a.B <= 0) return cudaSuccess;
-  // more rows than users: candidates, so the variants that take more rows of a user at once
+  // More rows than users: some user has several, so the variants that take more rows of a user
+  // at once.  Users without rows hide that, as the host knows R and B but no counts.  16
+  // candidates each of 3 users of 8192 rows, in a call of those users (wide) and of 64 (narrow):
+  // bf16 63 and 90 us (heads of 64, d 512), 129 and 157 (128, d 1024), e4m3 80 and 128 (128, d
+  // 1024), but 68 and 56 (64, d 512), fp32 146 and 205 (64, d 512).  With two rows a user, 8
+  // users of 2048: bf16 19 and 16 (d 512), 32 and 21 (d 1024), e4m3 24 and 20 (d 1024), fp32
+  // 19 and 25.  Callers leave idle users out where it counts, as runtime.PagedHistory.score does.
   const bool wide = a.R > a.B;
 #define HSTU_PAGES_ATTN(F, D) \
   return wide ? launch<F, D, (F == HSTU_PAGES_BF16 ? 3 : 2)>(a, st) : launch<F, D, 1>(a, st)

@@ -204,6 +204,11 @@ class PagedHistory:
         self.structs = [l.struct() for l in layers]
         self.table = torch.full((max_users, pages_per_user), -1, dtype=torch.int32, device=dev)
         self.lengths = torch.zeros(max_users, dtype=torch.int32, device=dev)
+        # rows of a user that the attention takes together in any call; e4m3 with heads of 64
+        # gains nothing by more
+        self.together = 1 if fmt == "fp32" else 2
+        if fmt == "e4m3" and c.head_dim == 64:
+            self.together = c.max_tokens
         self.held = [0] * max_users                       # lengths, on the host
         self.pages: List[List[int]] = [[] for _ in range(max_users)]
         self.free = list(range(num_pages - 1, -1, -1))
@@ -252,11 +257,14 @@ class PagedHistory:
             self.held[u] = n
         return out
 
-    def _step(self, counts, x, timestamps, out, append: bool) -> torch.Tensor:
+    def _step(self, counts, x, timestamps, out, append: bool, table=None,
+              lengths=None) -> torch.Tensor:
+        """One step of users with ``counts`` rows each: the slots, or those of ``table`` and
+        ``lengths``."""
+        table, lengths = (self.table, self.lengths) if table is None else (table, lengths)
         hstu.hstu_pages_step(self.handle.h, self.pools, x, x.shape[0], self._offsets(counts),
-                             len(self.held), timestamps, self.structs, self.table,
-                             self.table.shape[1], self.lengths, append, out,
-                             torch.cuda.current_stream(self.device))
+                             len(counts), timestamps, self.structs, table, self.table.shape[1],
+                             lengths, append, out, torch.cuda.current_stream(self.device))
         return out
 
     def append(self, slots, x: torch.Tensor, timestamps: torch.Tensor,
@@ -282,7 +290,15 @@ class PagedHistory:
         if len(counts) != len(self.held) or any(n < 0 for n in counts) or \
                 sum(counts) != x.shape[0]:
             raise ValueError("one count a slot, x.shape[0] rows in all")
-        return self._step(counts, x, timestamps, out, False)
+        busy = [u for u, n in enumerate(counts) if n > 0]
+        if not self.together * len(busy) < len(x) <= len(counts):
+            return self._step(counts, x, timestamps, out, False)
+        # several rows of some users, and no more rows than slots: only the users that have
+        # rows, since the attention takes more rows of a user together where a call has more
+        # rows than users
+        idx = torch.tensor(busy, dtype=torch.int64, device=self.device)
+        return self._step([counts[u] for u in busy], x, timestamps, out, False, self.table[idx],
+                          self.lengths[idx])
 
     def read(self, layer: int, slots):
         """(U|V|Q|K rows with the cached V and K and zeros elsewhere, timestamps) of ``slots``."""

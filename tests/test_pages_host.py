@@ -2,8 +2,13 @@
 without a GPU."""
 import os
 import re
+import types
 
-from jagged_pointwise_attention_hstu_b200 import build
+import numpy as np
+import pytest
+import torch
+
+from jagged_pointwise_attention_hstu_b200 import build, hstu, runtime
 
 
 def _source(name):
@@ -34,3 +39,77 @@ def test_a_warp_gives_up_a_wait_as_one():
     calls = re.findall(r"(?<!bool )\bwait_for\(", text)
     assert len(calls) == 1 and re.search(r"__all_sync\(0xffffffffu, wait_for\(", text)
     assert len(re.findall(r"(?<!bool )\bwait_by_all\(", text)) >= 4
+
+
+# ------------------------------------------------ runtime.PagedHistory over fake entry points
+
+D, H, PAGE = 128, 2, 16
+
+
+class _Cpu:
+    """torch, with the CPU where the owner asks for its GPU."""
+
+    class cuda:
+        current_stream = staticmethod(lambda device: None)
+
+    device = staticmethod(lambda *a: torch.device("cpu"))
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+
+class _Layer:
+    def struct(self):
+        return hstu.hstu_layer_weights()
+
+
+@pytest.fixture
+def owner(monkeypatch):
+    """A PagedHistory of five slots on the CPU, and what its entry points were given."""
+    calls = []
+
+    def record(*names):
+        def call(*args):
+            calls.append(dict(zip(names, args)))
+        return call
+
+    monkeypatch.setattr(runtime, "torch", _Cpu())
+    monkeypatch.setattr(hstu, "hstu_pages_step", record(
+        "h", "pools", "values", "R", "offsets", "B", "ts", "layers", "table", "width", "lengths",
+        "append", "out", "stream"))
+    monkeypatch.setattr(hstu, "hstu_pages_prefill", record(
+        "h", "pools", "values", "R", "offsets", "B", "ts", "layers", "table", "width", "out",
+        "stream"))
+    handle = types.SimpleNamespace(h=None, device=0, cfg=hstu.make_config(
+        D, H, io_dtype=hstu.HSTU_DTYPE_FP32, compute_dtype=hstu.HSTU_DTYPE_BF16, n_norm=64,
+        pos_buckets=129, pos_clamp=128, time_buckets=128, time_log_div=0.301, ln_eps=1e-5,
+        max_tokens=64, max_users=8))
+    hist = runtime.PagedHistory(handle, [_Layer()], num_pages=12, max_users=5, pages_per_user=4,
+                                page_size=PAGE)
+    return hist, calls
+
+
+def _rows(n):
+    return torch.zeros((n, D)), torch.zeros(n, dtype=torch.int64), torch.zeros((n, D))
+
+
+def test_score_passes_the_slots_that_have_candidates(owner):
+    """Idle slots do not count as users where that would hide that a user has several rows: the
+    attention takes them at once where there are more rows than users."""
+    hist, calls = owner
+    hist.prefill([3, 1], [20, 33], *_rows(53))
+    hist.score([0, 4, 0, 1, 0], *_rows(5))
+    c = calls[-1]
+    assert c["B"] == 2 and c["R"] == 5 and c["offsets"].tolist() == [0, 4, 5]
+    assert torch.equal(c["table"], hist.table[[1, 3]]) and c["lengths"].tolist() == [33, 20]
+    assert c["width"] == 4 and not c["append"] and c["table"].is_contiguous()
+    # no difference to the attention, or none for the better: the tables as they are
+    for counts in ([1, 2, 1, 1, 1], [0, 9, 0, 0, 0], [0, 2, 0, 1, 0], [0, 1, 0, 1, 0], [0] * 5):
+        hist.score(counts, *_rows(sum(counts)))
+        c = calls[-1]
+        assert c["B"] == 5 and c["offsets"].tolist()[1:] == np.cumsum(counts).tolist()
+        assert c["table"] is hist.table and c["lengths"] is hist.lengths
+    hist.append([1, 4], *_rows(2))
+    c = calls[-1]
+    assert c["B"] == 5 and c["offsets"].tolist() == [0, 0, 1, 1, 1, 2] and c["append"]
+    assert c["table"] is hist.table and hist.held == [0, 34, 0, 20, 1]
