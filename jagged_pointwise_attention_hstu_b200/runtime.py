@@ -247,11 +247,17 @@ class PagedHistory:
         if any(self.held[u] for u in slots):
             raise ValueError("a prefilled slot has to be empty: release it first")
         self._reserve(dict(zip(slots, counts)))
-        idx = torch.tensor(slots, dtype=torch.int64, device=self.device)
-        table = self.table[idx].contiguous()
-        hstu.hstu_pages_prefill(self.handle.h, self.pools, x, x.shape[0], self._offsets(counts),
-                                len(slots), timestamps, self.structs, table, table.shape[1], out,
-                                torch.cuda.current_stream(self.device))
+        try:
+            idx = torch.tensor(slots, dtype=torch.int64, device=self.device)
+            table = self.table[idx].contiguous()
+            hstu.hstu_pages_prefill(self.handle.h, self.pools, x, x.shape[0],
+                                    self._offsets(counts), len(slots), timestamps, self.structs,
+                                    table, table.shape[1], out,
+                                    torch.cuda.current_stream(self.device))
+        except Exception:
+            for u in reversed(slots):        # still empty: its pages are of no use to it
+                self._give_back(u)
+            raise
         self.lengths[idx] = torch.tensor(counts, dtype=torch.int32, device=self.device)
         for u, n in zip(slots, counts):
             self.held[u] = n
@@ -314,13 +320,16 @@ class PagedHistory:
                              torch.cuda.current_stream(self.device))
         return uvqk, ts
 
+    def _give_back(self, slot: int) -> None:
+        self.free += reversed(self.pages[slot])
+        self.pages[slot] = []
+        self.table[slot] = -1
+
     def release(self, slot: int) -> None:
         """Gives the slot's pages back."""
         slot, = self._slots([slot])
-        self.free += reversed(self.pages[slot])
-        self.pages[slot] = []
+        self._give_back(slot)
         self.held[slot] = 0
-        self.table[slot] = -1
         self.lengths[slot] = 0
 
 

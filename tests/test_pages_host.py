@@ -113,3 +113,21 @@ def test_score_passes_the_slots_that_have_candidates(owner):
     c = calls[-1]
     assert c["B"] == 5 and c["offsets"].tolist() == [0, 0, 1, 1, 1, 2] and c["append"]
     assert c["table"] is hist.table and hist.held == [0, 34, 0, 20, 1]
+
+
+def test_a_prefill_that_fails_gives_its_pages_back(owner, monkeypatch):
+    hist, _ = owner
+    hist.prefill([2], [17], *_rows(17))
+    free, table = list(hist.free), hist.table.clone()
+
+    def refuse(*args):
+        raise hstu.HstuError(hstu.HSTU_ERR_WORKSPACE, "hstu_pages_prefill")
+
+    with monkeypatch.context() as m:
+        m.setattr(hstu, "hstu_pages_prefill", refuse)
+        with pytest.raises(hstu.HstuError):
+            hist.prefill([0, 4], [64, 40], *_rows(104))
+    assert hist.free == free and torch.equal(hist.table, table)
+    assert hist.pages[0] == [] and hist.pages[4] == [] and hist.held == [0, 0, 17, 0, 0]
+    hist.prefill([1, 3], [64, 64], *_rows(128))          # all the pages but two
+    assert len(hist.free) == 2
