@@ -237,13 +237,25 @@ class PagedHistory:
             raise ValueError("slots are distinct numbers below max_users")
         return slots
 
+    def _check_rows(self, rows: int, x, timestamps, out) -> None:
+        c = self.handle.cfg
+        io = torch.bfloat16 if c.io_dtype == hstu.HSTU_DTYPE_BF16 else torch.float32
+        for what, t, shape, dtype in (("x", x, (rows, c.d_model), io),
+                                      ("timestamps", timestamps, (rows,), torch.int64),
+                                      ("out", out, (rows, c.d_model), io)):
+            if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device or \
+                    not t.is_contiguous():
+                raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {shape} on "
+                                 f"{self.device}")
+
     def prefill(self, slots, counts, x: torch.Tensor, timestamps: torch.Tensor,
                 out: torch.Tensor) -> torch.Tensor:
         """Runs the stack over the histories of empty ``slots`` (``counts`` rows each, packed in
         ``x``) and keeps them."""
         slots, counts = self._slots(slots), [int(n) for n in counts]
-        if len(counts) != len(slots) or any(n < 0 for n in counts) or sum(counts) != x.shape[0]:
-            raise ValueError("one count a slot, x.shape[0] rows in all")
+        if len(counts) != len(slots) or any(n < 0 for n in counts):
+            raise ValueError("one count a slot")
+        self._check_rows(sum(counts), x, timestamps, out)
         if any(self.held[u] for u in slots):
             raise ValueError("a prefilled slot has to be empty: release it first")
         self._reserve(dict(zip(slots, counts)))
@@ -277,8 +289,9 @@ class PagedHistory:
                out: torch.Tensor) -> torch.Tensor:
         """One new action for each of ``slots`` (ascending): row i of ``x`` is slots[i]'s."""
         slots = self._slots(slots)
-        if slots != sorted(slots) or len(slots) != x.shape[0]:
+        if slots != sorted(slots):
             raise ValueError("ascending slots, one row each")
+        self._check_rows(len(slots), x, timestamps, out)
         self._reserve({u: self.held[u] + 1 for u in slots})
         counts = [0] * len(self.held)
         for u in slots:
@@ -293,9 +306,9 @@ class PagedHistory:
               out: torch.Tensor) -> torch.Tensor:
         """Candidates of every slot (``counts``, one number a slot), packed in slot order."""
         counts = [int(n) for n in counts]
-        if len(counts) != len(self.held) or any(n < 0 for n in counts) or \
-                sum(counts) != x.shape[0]:
-            raise ValueError("one count a slot, x.shape[0] rows in all")
+        if len(counts) != len(self.held) or any(n < 0 for n in counts):
+            raise ValueError("one count a slot")
+        self._check_rows(sum(counts), x, timestamps, out)
         busy = [u for u, n in enumerate(counts) if n > 0]
         if not self.together * len(busy) < len(x) <= len(counts):
             return self._step(counts, x, timestamps, out, False)

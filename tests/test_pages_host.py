@@ -131,3 +131,28 @@ def test_a_prefill_that_fails_gives_its_pages_back(owner, monkeypatch):
     assert hist.pages[0] == [] and hist.pages[4] == [] and hist.held == [0, 0, 17, 0, 0]
     hist.prefill([1, 3], [64, 64], *_rows(128))          # all the pages but two
     assert len(hist.free) == 2
+
+
+@pytest.mark.parametrize("call", ["prefill", "append", "score"])
+def test_rows_that_the_library_would_take_for_others_are_refused(owner, call):
+    """Addresses reach the library without shapes: too few rows would be read or written out of
+    range, another type or order would be taken for this one."""
+    hist, calls = owner
+    hist.prefill([0, 1, 2], [5, 6, 7], *_rows(18))
+    held, free, n = list(hist.held), list(hist.free), len(calls)
+    run = {"prefill": lambda *rows: hist.prefill([3], [3], *rows),
+           "append": lambda *rows: hist.append([0, 1, 2], *rows),
+           "score": lambda *rows: hist.score([2, 0, 1, 0, 0], *rows)}[call]
+    x, ts, out = _rows(3)
+    for rows in ((x.bfloat16(), ts, out), (x, ts, out.bfloat16()), (x, ts.int(), out),
+                 (x, ts[:2], out), (x, ts, out[:2]), (x, ts, torch.zeros(4, D)),
+                 (torch.zeros(3, D + 8), ts, out), (torch.zeros(3, 2 * D)[:, :D], ts, out),
+                 (x, torch.zeros(3, 2, dtype=torch.int64)[:, 0], out),
+                 (x, ts, torch.zeros(D, 3).T), (x, ts, out.to("meta")), (x[None], ts, out),
+                 (torch.zeros(2, D), ts, out)):
+        with pytest.raises(ValueError):
+            run(*rows)
+    assert len(calls) == n and hist.held == held and hist.free == free
+    run(x, ts, out)
+    run(x, ts, x) if call != "prefill" else None         # in place
+    assert len(calls) > n
