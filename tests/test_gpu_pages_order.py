@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 def test_rows_that_move_from_page_to_page(fmt, d, H, ps, users, n, how):
     """Every user's rows read into one buffer and written at once over the next user's pages, and
     the attention over them, thirteen times: pages, buffer and results are those of the same calls
-    with a wait after each.  Small grids, of which several kernels fit the GPU at once, and large."""
+    with a wait after each.  Small grids, of which the GPU holds several at once, and large ones."""
     R, steps = users * n, 13                            # no multiple of a case's users
     h = _handle(d, H, fmt, rows=R)
     pool = _filled(h, d, H, fmt, ps, [n] * users, seed=90)

@@ -14,6 +14,7 @@ from oracle import paged_history as ph
 from jagged_pointwise_attention_hstu_b200 import build, hstu
 
 from helpers import oracle_cfg
+from pages_marks import marks
 
 
 @pytest.fixture(scope="module")
@@ -156,3 +157,22 @@ def test_bindings_take_tensors_and_addresses_and_nothing_else():
             hstu._stream_ptr(bad)
     with pytest.raises(AttributeError):
         hstu._stream_ptr(x)
+
+
+@pytest.mark.parametrize("columns", [32, 64, 128])
+@pytest.mark.parametrize("n", [1, 64, 129, 700, 9001, 50_001, 100_003])
+def test_a_run_of_positions_lost_or_summed_twice_shows_in_the_marks(n, columns):
+    """What the GPU test of joined histories compares: leaving out a unit of 64 or 128
+    positions (a part's first, last or any other) or a single one, or taking one in place of
+    another, changes the sums, whichever column of the keys a row asks for."""
+    i = torch.arange(n)
+    v, k = marks(i, columns), marks(i + 100_003, columns)
+    for column in (0, 1, 9, 20, columns - 1):
+        terms = (1 + k[:, column])[:, None] * v          # the smallest biases
+        for unit in (1, 64, 128):
+            parts = torch.zeros((-(-n // unit) * unit, columns), dtype=torch.int64)
+            parts[:n] = terms
+            parts = parts.view(-1, unit, columns).sum(1)
+            assert torch.all(parts[:, 0] > 0)
+            assert len(torch.unique(parts, dim=0)) == len(parts)
+    assert 4 * n + 8 < 2 ** 24
