@@ -50,8 +50,8 @@ typedef struct {
  *   total_rows   R, 0 <= R <= max_tokens: rows of the call's [R, *] tensors
  *   seq_offsets  device int32 [num_users + 1], 0 = offsets[0] <= ... <= offsets[B] <= R:
  *                user b owns rows offsets[b] .. offsets[b+1]-1 (none is allowed).  Rows from
- *                offsets[B] on (the padding of a launch of fixed size) are not read, and
- *                their outputs are left as they were
+ *                offsets[B] on (the padding of a launch of fixed size) have to be readable,
+ *                but their values reach nothing, and their outputs are left as they were
  *   page_table   device int32 [num_users, table_width]; entries that no position of the call
  *                needs are not read.  table_width * page_size <= 2^30
  * The calls work on the rows, pages and tables as they are in stream order, so
@@ -62,13 +62,14 @@ typedef struct {
  * skipped and its outputs are undefined (offsets that fall or leave the rows
  * concern every user: the attention then writes nothing).
  *
- * The attention uses the handle's workspace: the calls of one handle, and the
- * replays of its captured calls, must not overlap.  Its waits are bounded as
- * hstu_set_wait_limit says; one that expires sets HSTU_DEVERR_TIMEOUT, and the
- * handle's attention over pages is undefined until hstu_get_device_error has been
- * called.  Infinities and NaN among the q, k and v of a row or the keys and values it
- * sees make its outputs of that head non-finite or NaN, not more; so do finite ones with
- * a score, or (E4M3) a SiLU(score) * 2^e of a value's block, that fp32 does not hold. */
+ * The attention uses the handle's workspace (32 KB an SM in every handle, 4.8 MB on a
+ * B200): the calls of one handle, and the replays of its captured calls, must not
+ * overlap.  Its waits are bounded as hstu_set_wait_limit says; one that expires sets
+ * HSTU_DEVERR_TIMEOUT, and the handle's attention over pages is undefined until
+ * hstu_get_device_error has been called.  Infinities and NaN among the q, k and v of a row
+ * or the keys and values it sees make its outputs of that head non-finite or NaN, not more;
+ * so do finite ones with a score, or (E4M3) a SiLU(score) * 2^e of a value's block, that
+ * fp32 does not hold. */
 
 /* Writes (and quantises) rows into pages: row offsets[b] + i of `uvqk` becomes
  * position start[b] + i of user b.

@@ -201,7 +201,7 @@ struct Chunks {
 // and nearly by its instructions.  All of a lane's loads (8, whatever d is) are on their
 // way before the rows' places are looked up; the scale bytes of eight rows are
 // gathered and stored as one where they are neighbours, since a store of one byte
-// costs as much as one of 32.  65536 rows of d 1024 to e4m3 pages: 74 us, 5.5 TB/s (149
+// costs as much as one of 32.  65536 rows of d 1024 to e4m3 pages: 73 us, 5.6 TB/s (149
 // with one load at a time and 25 instructions a value, 12 now; 78 with a store a scale
 // byte; 65.6 with nothing to compute).
 template <int FMT, int HD, int ROWS>
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) pages_read_kernel(const PagesA
 
 // Rows of a warp: one, or as many as a batch of loads covers once there are more rows than
 // warps the GPU holds (64 an SM): 64 users of up to 1024 rows, d 256, e4m3 are written in
-// 6.8 us (10.1 with one row a warp) and read in 5.9 (8.7), 191 of up to 293, d 64, fp32 in 4.0
+// 6.8 us (10.1 with one row a warp) and read in 6.1 (8.7), 191 of up to 293, d 64, fp32 in 4.0
 // (7.4) and 5.1 (7.0); with fewer rows than warps the latency of a row counts, 16 users of up
 // to 1024, d 256, bf16 3.8 us to read with four rows a warp and 3.1 with one.  Heads of 96 have
 // 96 chunks a row at least.

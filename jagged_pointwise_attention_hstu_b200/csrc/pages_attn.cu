@@ -38,11 +38,12 @@
 // straight into registers and fp32 arithmetic.
 //
 // Measured (B200, warm calls, a call's share of a graph of 21): 8 users of 8192 rows, d 1024,
-// bf16 49.5 us (5.4 TB/s); 256 of 4096, d 512, e4m3 187 to 201 us (5.5 to 5.9 TB/s; 175
+// bf16 49.3 us (5.5 TB/s); 256 of 4096, d 512, e4m3 183 to 201 us (5.5 to 6.0 TB/s; 175
 // with the arithmetic left out); 168 of 2080, d 768, bf16 167 us (6.4 TB/s); 1 of 100003,
-// d 512, e4m3 26.1 us (4.0 TB/s: the start takes 4 us, the join 3); 1 of 37, d 256 5.4 us.
+// d 512, e4m3 26.1 us (4.0 TB/s: the start takes 4 us, the join 3); 1 of 37, d 256 5.3 us.
 // What bounds e4m3 at head dim 64 besides memory is the latency of the 12 warps an SM holds
-// (a step of 32 keys is 230 instructions, 66 of them conversions).
+// (a step of 32 keys is 382 instructions: 146 are waits and book-keeping, 236 the arithmetic,
+// 67 of those conversions).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -170,7 +171,7 @@ __device__ __forceinline__ User user_of(const PagesArgs& a, int32_t b, int& err)
 // Parts, if every block can have one part of one segment, of at most `share`
 // units: then it does, the segments cut into equal parts.  Else runs: block c has
 // the units from c * share on, whatever segments they belong to; but a segment of
-// at most share / 8 units is not cut, the block it begins in takes it whole.  A cut
+// at most share / 8 units is not cut, the block it ends in takes it whole.  A cut
 // costs the join of its parts (2 to 3 us: the parts' way to memory, a ticket, the
 // parts' way back), as much as a few units, and a block with the ends of two
 // segments pays for two.  (16 users of up to 4096 rows, d 512: runs 15.9 us,
