@@ -239,15 +239,18 @@ class PagedHistory:
         return slots
 
     def _check_rows(self, rows: int, x, timestamps, out) -> None:
+        """``x`` has the call's rows; ``timestamps`` and ``out`` may have more (buffers of a fixed
+        size)."""
         c = self.handle.cfg
         io = torch.bfloat16 if c.io_dtype == hstu.HSTU_DTYPE_BF16 else torch.float32
-        for what, t, shape, dtype in (("x", x, (rows, c.d_model), io),
-                                      ("timestamps", timestamps, (rows,), torch.int64),
-                                      ("out", out, (rows, c.d_model), io)):
-            if tuple(t.shape) != shape or t.dtype != dtype or t.device != self.device or \
-                    not t.is_contiguous():
-                raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {shape} on "
-                                 f"{self.device}")
+        for what, t, width, dtype in (("x", x, (c.d_model,), io),
+                                      ("timestamps", timestamps, (), torch.int64),
+                                      ("out", out, (c.d_model,), io)):
+            if t.dim() != 1 + len(width) or tuple(t.shape[1:]) != width or t.shape[0] < rows or \
+                    (t is x and t.shape[0] != rows) or t.dtype != dtype or \
+                    t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{what}: a contiguous {dtype} tensor of {rows} rows of "
+                                 f"{width} on {self.device}")
 
     def prefill(self, slots, counts, x: torch.Tensor, timestamps: torch.Tensor,
                 out: torch.Tensor) -> torch.Tensor:

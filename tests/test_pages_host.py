@@ -145,8 +145,8 @@ def test_rows_that_the_library_would_take_for_others_are_refused(owner, call):
            "score": lambda *rows: hist.score([2, 0, 1, 0, 0], *rows)}[call]
     x, ts, out = _rows(3)
     for rows in ((x.bfloat16(), ts, out), (x, ts, out.bfloat16()), (x, ts.int(), out),
-                 (x, ts[:2], out), (x, ts, out[:2]), (x, ts, torch.zeros(4, D)),
-                 (torch.zeros(3, D + 8), ts, out), (torch.zeros(3, 2 * D)[:, :D], ts, out),
+                 (x, ts[:2], out), (x, ts, out[:2]), (torch.zeros(4, D), ts, out),
+                 (torch.zeros(3, D + 8), ts, out), (x, ts, torch.zeros(3, D + 8)), (torch.zeros(3, 2 * D)[:, :D], ts, out),
                  (x, torch.zeros(3, 2, dtype=torch.int64)[:, 0], out),
                  (x, ts, torch.zeros(D, 3).T), (x, ts, out.to("meta")), (x[None], ts, out),
                  (torch.zeros(2, D), ts, out)):
@@ -154,5 +154,7 @@ def test_rows_that_the_library_would_take_for_others_are_refused(owner, call):
             run(*rows)
     assert len(calls) == n and hist.held == held and hist.free == free
     run(x, ts, out)
-    run(x, ts, x) if call != "prefill" else None         # in place
-    assert len(calls) > n
+    if call != "prefill":
+        run(x, ts, x)                                    # in place
+        run(x, torch.zeros(9, dtype=torch.int64), torch.zeros(7, D))   # buffers of a fixed size
+    assert len(calls) == n + (1 if call == "prefill" else 3)
